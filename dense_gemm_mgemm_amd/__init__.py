@@ -25,7 +25,9 @@ KERNELS = ["auto", "general", "f32_mfma", "h_mfma_256x256", "h_mfma_256x192", "h
            "skinny", "reserved_7", "f32_fast", "f32_fast_128",
            "h_dma_256x256", "skinny_sk", "h_dma_256x192", "f32_fast_u",
            "f8_mfma_256x256", "f8_general", "f8_mfma_256x192", "f32_sk", "h_dma_128x192",
-           "h_dma_64x192", "f8_mfma_128x192"]
+           "h_dma_64x192", "f8_mfma_128x192",
+           "mx4_general", "mx4_skinny", "mx4_mfma_256x256", "mx4_mfma_256x192", "mx4_mfma_128x192",
+           "mx4_mfma_64x192"]
 MGEMM_KERNEL_AUTO = 0
 MGEMM_EPILOGUE_NONE, MGEMM_EPILOGUE_SILU = 0, 1
 _EPILOGUE = {"none": MGEMM_EPILOGUE_NONE, "silu": MGEMM_EPILOGUE_SILU}
@@ -39,7 +41,8 @@ EXPORTED = ["mgemm_create", "mgemm_destroy", "mgemm_run", "mgemm_run_kernel", "m
             "mgemm_table_clear", "mgemm_weighted_choice", "mgemm_quantize_fp8", "mgemm_run_fp8",
             "mgemm_status_string",
             "mgemm_kernel_name", "mgemm_num_cu", "mgemm_run_noalloc", "mgemm_set_clock_stamps",
-            "mgemm_run_acc32"]
+            "mgemm_run_acc32", "mgemm_quantize_mx4", "mgemm_dequantize_mx4", "mgemm_run_mx4",
+            "mgemm_linear_mx4", "mgemm_gated_mx4"]
 
 
 class MgemmError(RuntimeError):
@@ -107,6 +110,16 @@ def load(path: str | None = None):
         getattr(lib, name).restype = ci
     lib.mgemm_run_acc32.argtypes = [vp, ci, ci, ci, i64, i64, i64, f32, vp, i64, vp, i64, vp, i64,
                                     ci, vp]
+    lib.mgemm_quantize_mx4.argtypes = [vp, i64, i64, vp, i64, ci, vp, i64, vp, i64, vp]
+    lib.mgemm_dequantize_mx4.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64, ci, vp]
+    lib.mgemm_run_mx4.argtypes = [vp, ci, ctypes.c_int32, i64, i64, i64, f32, vp, i64, vp, i64, vp,
+                                  i64, vp, i64, f32, vp, i64, ci, vp]
+    lib.mgemm_linear_mx4.argtypes = [vp, i64, i64, i64, vp, i64, ci, vp, i64, vp, i64, vp, i64, ci, vp]
+    lib.mgemm_gated_mx4.argtypes = [vp, i64, i64, i64, vp, i64, ci, vp, vp, vp, vp, i64, i64, vp, i64,
+                                    ci, vp]
+    for name in ("mgemm_quantize_mx4", "mgemm_dequantize_mx4", "mgemm_run_mx4", "mgemm_linear_mx4",
+                 "mgemm_gated_mx4"):
+        getattr(lib, name).restype = ci
     lib.mgemm_status_string.argtypes = [ci]
     lib.mgemm_status_string.restype = ctypes.c_char_p
     lib.mgemm_kernel_name.argtypes = [ci]
@@ -335,6 +348,54 @@ def mgemm_run_fp8(h, kernel, M, N, K, alpha, A, lda, sa, B, ldb, sb, beta, C, ld
                               _ptr(C), int(ldc), _enum(ctype, _DTYPE), _stream(stream))
     if st != MGEMM_SUCCESS:
         raise MgemmError(st, "mgemm_run_fp8(%s, %d)" % (kernel, ksplit))
+
+
+def mgemm_quantize_mx4(h, M, K, X, ldx, xtype, Q, ldq, S, lds, stream=None) -> None:
+    """X (M x K) to MX4 codes Q (row stride ldq bytes) and scale bytes S (row stride lds)."""
+    st = load().mgemm_quantize_mx4(h, int(M), int(K), _ptr(X), int(ldx), _enum(xtype, _DTYPE), _ptr(Q),
+                                   int(ldq), _ptr(S), int(lds), _stream(stream))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_quantize_mx4")
+
+
+def mgemm_dequantize_mx4(h, M, K, Q, ldq, S, lds, Y, ldy, ytype, stream=None) -> None:
+    """The values that MX4 codes and scales stand for, into Y (M x K)."""
+    st = load().mgemm_dequantize_mx4(h, int(M), int(K), _ptr(Q), int(ldq), _ptr(S), int(lds), _ptr(Y),
+                                     int(ldy), _enum(ytype, _DTYPE), _stream(stream))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_dequantize_mx4")
+
+
+def mgemm_run_mx4(h, kernel, M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, C, ldc, ctype,
+                  stream=None, ksplit=0) -> None:
+    """C = alpha * A B^T + beta * C on MX4 codes and scales (ksplit: 0 = the
+    library's choice, 1 = no split, n = at most n K ranges)."""
+    k = KERNELS.index(kernel) if isinstance(kernel, str) else int(kernel)
+    st = load().mgemm_run_mx4(h, k, int(ksplit), int(M), int(N), int(K), float(alpha), _ptr(A), int(lda),
+                              _ptr(SA), int(ldsa), _ptr(B), int(ldb), _ptr(SB), int(ldsb), float(beta),
+                              _ptr(C), int(ldc), _enum(ctype, _DTYPE), _stream(stream))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_run_mx4(%s, %d)" % (kernel, ksplit))
+
+
+def mgemm_linear_mx4(h, M, N, K, X, ldx, xtype, B, ldb, SB, ldsb, Y, ldy, ytype, stream=None) -> None:
+    """Y = Q(X) B^T: MX4 weights (N x K), activations quantised within the call."""
+    st = load().mgemm_linear_mx4(h, int(M), int(N), int(K), _ptr(X), int(ldx), _enum(xtype, _DTYPE),
+                                 _ptr(B), int(ldb), _ptr(SB), int(ldsb), _ptr(Y), int(ldy),
+                                 _enum(ytype, _DTYPE), _stream(stream))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_linear_mx4")
+
+
+def mgemm_gated_mx4(h, M, N, K, X, ldx, xtype, Bg, SBg, Bu, SBu, ldb, ldsb, Z, ldz, ztype,
+                    stream=None) -> None:
+    """Z = SiLU(Q(X) Bg^T) * (Q(X) Bu^T): MX4 weights (N x K each), activations
+    quantised within the call."""
+    st = load().mgemm_gated_mx4(h, int(M), int(N), int(K), _ptr(X), int(ldx), _enum(xtype, _DTYPE),
+                                _ptr(Bg), _ptr(SBg), _ptr(Bu), _ptr(SBu), int(ldb), int(ldsb), _ptr(Z),
+                                int(ldz), _enum(ztype, _DTYPE), _stream(stream))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_gated_mx4")
 
 
 def mgemm_select_kernel(h, layoutA, layoutB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc,

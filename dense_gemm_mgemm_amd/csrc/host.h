@@ -61,6 +61,9 @@ bool variant_supports(const Problem& p, mgemm_kernel_t k);
 // Number of K ranges a forced kernel runs with for a request (0 = its own
 // choice); 0 when it cannot run them.
 int forced_splits(const Problem& p, const mgemm::Workspace& ws, mgemm_kernel_t k, int requested);
+// Predicted time (microseconds) of a 16-bit MFMA kernel (mgemm_api.cpp).
+double predict_us(const Problem& p, int bm, int bn, int out_n, double speed, int per_cu, int ks,
+                  double part_rate = 0.0);
 // The built-in time model's choice.
 Choice model_choice(const Problem& p, const mgemm::Workspace& ws);
 // Table entry, else the model.

@@ -116,7 +116,7 @@ bool variant_supports(const Problem& p, mgemm_kernel_t k) {
 // 0.25-0.27 us per slice, above their share of the MFMA time).  `part_rate`
 // replaces the partials' 2.6 TB/s where a caller measured its own.
 double predict_us(const Problem& p, int bm, int bn, int out_n, double speed, int per_cu, int ks,
-                  double part_rate = 0.0) {
+                  double part_rate) {
     constexpr double SLICE_US = 0.98, WG_US = 2.0, PASS_US = 4.0;
     const double PART_BYTES_PER_US = part_rate > 0.0 ? part_rate : 2.6e6;
     constexpr double CU_BYTES_PER_US = 60e3;
@@ -799,6 +799,12 @@ const char* mgemm_kernel_name(mgemm_kernel_t k) {
     case MGEMM_KERNEL_F32_SK: return "f32_sk";
     case MGEMM_KERNEL_H_DMA_128: return "h_dma_128x192";
     case MGEMM_KERNEL_H_DMA_64: return "h_dma_64x192";
+    case MGEMM_KERNEL_MX4_GENERAL: return "mx4_general";
+    case MGEMM_KERNEL_MX4_SKINNY: return "mx4_skinny";
+    case MGEMM_KERNEL_MX4_MFMA: return "mx4_mfma_256x256";
+    case MGEMM_KERNEL_MX4_MFMA_192: return "mx4_mfma_256x192";
+    case MGEMM_KERNEL_MX4_MFMA_128: return "mx4_mfma_128x192";
+    case MGEMM_KERNEL_MX4_MFMA_64: return "mx4_mfma_64x192";
     default: return "unknown";
     }
 }

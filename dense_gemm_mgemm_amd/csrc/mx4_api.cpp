@@ -1,0 +1,233 @@
+// Entry points of the microscaled 4-bit format: argument checks, kernel
+// choice, and the workspace of activations quantised within a call.  See
+// include/mgemm.h for the contracts.
+#include <hip/hip_runtime.h>
+
+#include "host.h"
+#include "mx4.h"
+
+using namespace mgemm_host;
+
+namespace {
+
+using mgemm::Mx4Args;
+using mgemm::Workspace;
+
+constexpr int64_t LIM = (int64_t)1 << 62;
+
+bool valid_dtype(mgemm_dtype_t d) { return d == MGEMM_F32 || d == MGEMM_F16 || d == MGEMM_BF16; }
+int64_t max1(int64_t x) { return x > 1 ? x : 1; }
+mgemm_status_t status(hipError_t e) { return e == hipSuccess ? MGEMM_SUCCESS : MGEMM_ERR_HIP; }
+
+// Whether rows x K values with element stride ld can be addressed.
+bool valid_matrix(int64_t rows, int64_t K, int64_t ld) {
+    return ld >= max1(K) && (rows == 0 || ld <= LIM / rows);
+}
+// The same for a matrix of codes and scales with byte strides.
+bool valid_mx4(int64_t rows, int64_t K, int64_t ldq, int64_t lds) {
+    if (K > LIM / 2) return false;
+    const int64_t nb = mgemm::mx4_blocks(K);
+    return ldq >= max1(16 * nb) && lds >= max1(nb) && (rows == 0 || (ldq <= LIM / rows && lds <= LIM / rows));
+}
+
+Problem problem(mgemm_handle_t h, int64_t M, int64_t N, int64_t K, void* C, int64_t ldc, mgemm_dtype_t ctype) {
+    Problem p{};
+    p.M = M; p.N = N; p.K = K;
+    p.alpha = 1.0f;
+    p.a_kc = p.b_kc = 1;
+    p.C = C; p.ldc = ldc;
+    p.dtype = (int)ctype;
+    p.num_cu = h->num_cu;
+    p.epilogue = mgemm::EPI_NONE;
+    p.stamps = h->stamps;
+    p.stamps_cap = h->stamps ? h->stamps_cap : 0;
+    return p;
+}
+
+struct Tile {
+    int bn, bm, ks;
+};
+struct Shape {
+    mgemm_kernel_t kernel;
+    int bn, bm;
+};
+constexpr Shape SHAPES[] = {{MGEMM_KERNEL_MX4_MFMA, 256, 256},
+                            {MGEMM_KERNEL_MX4_MFMA_192, 192, 256},
+                            {MGEMM_KERNEL_MX4_MFMA_128, 192, 128},
+                            {MGEMM_KERNEL_MX4_MFMA_64, 192, 64}};
+
+// The split with the smallest predicted time for one tile shape.  A
+// 128-element slice moves the bytes and takes the matrix time of a 32-element
+// slice of a 16-bit product, so the 16-bit time model applies to K / 4, with the
+// partials priced as for FP8.
+Tile best_split(const Problem& p, int bn, int bm, const Workspace& ws, double* t_out) {
+    Problem q = p;
+    q.K = p.K / 4;
+    const int out = p.B2 != nullptr ? 96 : bn;
+    Tile best{bn, bm, 1};
+    double bt = 1e300;
+    for (int req = 1, last = 0; req <= MGEMM_MAX_KSPLIT; ++req) {
+        const int ks = mgemm::mx4_splits(p, bn, bm, req, ws);
+        if (ks <= last) continue;
+        last = ks;
+        const double t = predict_us(q, bm, bn, out, bn == 256 ? 1.4 : 1.3, 1, ks, 4.5e6);
+        if (t < bt) { bt = t; best.ks = ks; }
+    }
+    *t_out = bt;
+    return best;
+}
+
+// Launches a product of codes: forced kernel or the library's choice.
+mgemm_status_t launch(const Problem& p, const Mx4Args& a, mgemm_kernel_t kernel, int ksplit, const Workspace& ws,
+                      hipStream_t s) {
+    if (kernel == MGEMM_KERNEL_MX4_GENERAL || kernel == MGEMM_KERNEL_MX4_SKINNY) {
+        if (ksplit > 1) return MGEMM_ERR_UNSUPPORTED;
+        if (kernel == MGEMM_KERNEL_MX4_GENERAL) return status(mgemm::launch_mx4_general(p, a, s));
+        if (!mgemm::mx4_skinny_supports(p, a)) return MGEMM_ERR_UNSUPPORTED;
+        return status(mgemm::launch_mx4_skinny(p, a, s));
+    }
+    Tile best{0, 0, 0};
+    double best_t = 1e300;
+    for (const Shape& c : SHAPES) {
+        if (kernel != MGEMM_KERNEL_AUTO && kernel != c.kernel) continue;
+        if (!mgemm::mx4_mfma_supports(p, a, c.bn, c.bm)) continue;
+        double t;
+        const Tile tile = best_split(p, c.bn, c.bm, ws, &t);
+        if (t < best_t) { best_t = t; best = tile; }
+    }
+    if (kernel == MGEMM_KERNEL_AUTO) {
+        if (p.M <= 64 && mgemm::mx4_skinny_supports(p, a)) return status(mgemm::launch_mx4_skinny(p, a, s));
+        if (best.bn == 0) return status(mgemm::launch_mx4_general(p, a, s));
+    }
+    if (best.bn == 0) return MGEMM_ERR_UNSUPPORTED;
+    if (ksplit > 0) best.ks = mgemm::mx4_splits(p, best.bn, best.bm, ksplit, ws);
+    if (best.ks < 1) return MGEMM_ERR_UNSUPPORTED;
+    return status(mgemm::launch_mx4_mfma(p, a, best.bn, best.bm, best.ks, ws, s));
+}
+
+// Y (or Z: p.B2 set) from activations: quantised inside the decode kernel, or
+// into the workspace a band of rows at a time.
+mgemm_status_t from_values(mgemm_handle_t h, Problem p, Mx4Args a, hipStream_t s) {
+    const int es = a.xtype == mgemm::F32 ? 4 : 2, cs = p.dtype == mgemm::F32 ? 4 : 2;
+    if (mgemm::mx4_skinny_supports(p, a)) return status(mgemm::launch_mx4_skinny(p, a, s));
+    // Codes and scales take the front half of the workspace, split-K partials the rest.
+    const int64_t nb = mgemm::mx4_blocks(p.K), ldq = 16 * nb, lds = (nb + 15) / 16 * 16;
+    const int64_t half = h->ws.part_bytes / 2;
+    int64_t band = half / (ldq + lds);
+    if (band < 1) return MGEMM_ERR_UNSUPPORTED;
+    if (band > 256) band = band / 256 * 256;
+    Workspace rest = h->ws;
+    rest.part = (char*)h->ws.part + half;
+    rest.part_bytes -= half;
+    const char* X = (const char*)a.X;
+    char* C = (char*)p.C;
+    const int64_t M = p.M;
+    uint8_t* q = (uint8_t*)h->ws.part;
+    a.X = nullptr;
+    p.A = q;
+    p.lda = ldq;
+    a.ldsa = lds;
+    for (int64_t m = 0; m < M; m += band) {
+        p.M = M - m < band ? M - m : band;
+        uint8_t* sc = q + p.M * ldq;
+        a.sa = sc;
+        p.C = C + m * p.ldc * cs;
+        hipError_t e = mgemm::launch_quantize_mx4(p.M, p.K, X + m * a.ldx * es, a.ldx, a.xtype, q, ldq, sc, lds, s);
+        if (e != hipSuccess) return MGEMM_ERR_HIP;
+        const mgemm_status_t st = launch(p, a, MGEMM_KERNEL_AUTO, 0, rest, s);
+        if (st != MGEMM_SUCCESS) return st;
+    }
+    return MGEMM_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+mgemm_status_t mgemm_quantize_mx4(mgemm_handle_t h, int64_t M, int64_t K, const void* X, int64_t ldx,
+                                  mgemm_dtype_t xtype, void* Q, int64_t ldq, void* S, int64_t lds,
+                                  hipStream_t stream) {
+    if (!h || M < 0 || K < 0 || !valid_dtype(xtype)) return MGEMM_ERR_INVALID_ARG;
+    if (!valid_matrix(M, K, ldx) || !valid_mx4(M, K, ldq, lds)) return MGEMM_ERR_INVALID_ARG;
+    if (M == 0 || K == 0) return MGEMM_SUCCESS;
+    if (!X || !Q || !S) return MGEMM_ERR_INVALID_ARG;
+    if (K > (int64_t)1 << 33) return MGEMM_ERR_UNSUPPORTED;
+    return status(mgemm::launch_quantize_mx4(M, K, X, ldx, (int)xtype, (uint8_t*)Q, ldq, (uint8_t*)S, lds, stream));
+}
+
+mgemm_status_t mgemm_dequantize_mx4(mgemm_handle_t h, int64_t M, int64_t K, const void* Q, int64_t ldq,
+                                    const void* S, int64_t lds, void* Y, int64_t ldy, mgemm_dtype_t ytype,
+                                    hipStream_t stream) {
+    if (!h || M < 0 || K < 0 || !valid_dtype(ytype)) return MGEMM_ERR_INVALID_ARG;
+    if (!valid_matrix(M, K, ldy) || !valid_mx4(M, K, ldq, lds)) return MGEMM_ERR_INVALID_ARG;
+    if (M == 0 || K == 0) return MGEMM_SUCCESS;
+    if (!Q || !S || !Y) return MGEMM_ERR_INVALID_ARG;
+    if (K > (int64_t)1 << 33) return MGEMM_ERR_UNSUPPORTED;
+    return status(mgemm::launch_dequantize_mx4(M, K, (const uint8_t*)Q, ldq, (const uint8_t*)S, lds, Y, ldy,
+                                               (int)ytype, stream));
+}
+
+mgemm_status_t mgemm_run_mx4(mgemm_handle_t h, mgemm_kernel_t kernel, int32_t ksplit, int64_t M, int64_t N,
+                             int64_t K, float alpha, const void* A, int64_t lda, const void* SA, int64_t ldsa,
+                             const void* B, int64_t ldb, const void* SB, int64_t ldsb, float beta, void* C,
+                             int64_t ldc, mgemm_dtype_t ctype, hipStream_t stream) {
+    if (!h || M < 0 || N < 0 || K < 0 || !valid_dtype(ctype)) return MGEMM_ERR_INVALID_ARG;
+    if (ksplit < 0 || ksplit > MGEMM_MAX_KSPLIT || (kernel == MGEMM_KERNEL_AUTO && ksplit != 0))
+        return MGEMM_ERR_INVALID_ARG;
+    if (kernel != MGEMM_KERNEL_AUTO && (kernel < MGEMM_KERNEL_MX4_GENERAL || kernel > MGEMM_KERNEL_MX4_MFMA_64))
+        return MGEMM_ERR_INVALID_ARG;
+    if (!valid_mx4(M, K, lda, ldsa) || !valid_mx4(N, K, ldb, ldsb) || !valid_matrix(M, N, ldc))
+        return MGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return MGEMM_SUCCESS;
+    if (!C) return MGEMM_ERR_INVALID_ARG;
+    Problem p = problem(h, M, N, K, C, ldc, ctype);
+    p.alpha = alpha;
+    p.beta = beta;
+    if (K == 0 || alpha == 0.f) return status(mgemm::launch_scale(p, stream));
+    if (!A || !SA || !B || !SB) return MGEMM_ERR_INVALID_ARG;
+    p.A = A; p.lda = lda;
+    p.B = B; p.ldb = ldb;
+    Mx4Args a{};
+    a.sa = (const uint8_t*)SA; a.ldsa = ldsa;
+    a.sb = (const uint8_t*)SB; a.ldsb = ldsb;
+    return launch(p, a, kernel, ksplit, h->ws, stream);
+}
+
+mgemm_status_t mgemm_linear_mx4(mgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                                mgemm_dtype_t xtype, const void* B, int64_t ldb, const void* SB, int64_t ldsb,
+                                void* Y, int64_t ldy, mgemm_dtype_t ytype, hipStream_t stream) {
+    if (!h || M < 0 || N < 0 || K < 0 || !valid_dtype(xtype) || !valid_dtype(ytype)) return MGEMM_ERR_INVALID_ARG;
+    if (!valid_matrix(M, K, ldx) || !valid_mx4(N, K, ldb, ldsb) || !valid_matrix(M, N, ldy))
+        return MGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return MGEMM_SUCCESS;
+    if (!Y) return MGEMM_ERR_INVALID_ARG;
+    Problem p = problem(h, M, N, K, Y, ldy, ytype);
+    if (K == 0) return status(mgemm::launch_scale(p, stream));
+    if (!X || !B || !SB) return MGEMM_ERR_INVALID_ARG;
+    p.B = B; p.ldb = ldb;
+    Mx4Args a{};
+    a.sb = (const uint8_t*)SB; a.ldsb = ldsb;
+    a.X = X; a.ldx = ldx; a.xtype = (int)xtype;
+    return from_values(h, p, a, stream);
+}
+
+mgemm_status_t mgemm_gated_mx4(mgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                               mgemm_dtype_t xtype, const void* Bg, const void* SBg, const void* Bu,
+                               const void* SBu, int64_t ldb, int64_t ldsb, void* Z, int64_t ldz,
+                               mgemm_dtype_t ztype, hipStream_t stream) {
+    if (!h || M < 0 || N < 0 || K < 0 || !valid_dtype(xtype) || !valid_dtype(ztype)) return MGEMM_ERR_INVALID_ARG;
+    if (!valid_matrix(M, K, ldx) || !valid_mx4(N, K, ldb, ldsb) || !valid_matrix(M, N, ldz))
+        return MGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return MGEMM_SUCCESS;
+    if (!Z) return MGEMM_ERR_INVALID_ARG;
+    Problem p = problem(h, M, N, K, Z, ldz, ztype);
+    if (K == 0) return status(mgemm::launch_scale(p, stream));   // G = U = 0
+    if (!X || !Bg || !SBg || !Bu || !SBu) return MGEMM_ERR_INVALID_ARG;
+    p.B = Bg; p.B2 = Bu; p.ldb = p.ldb2 = ldb;
+    Mx4Args a{};
+    a.sb = (const uint8_t*)SBg; a.sb2 = (const uint8_t*)SBu; a.ldsb = ldsb;
+    a.X = X; a.ldx = ldx; a.xtype = (int)xtype;
+    return from_values(h, p, a, stream);
+}
+
+}  // extern "C"

@@ -91,7 +91,13 @@ typedef enum {
     MGEMM_KERNEL_F8_MFMA_128 = 20, /* FP8 codes (mgemm_run_fp8 only): 128x192 tiles, 4 waves of
                                       64x96, f8f6f4 MFMA (grids of 256-row tiles that leave CUs
                                       idle) */
-    MGEMM_KERNEL_COUNT = 21
+    MGEMM_KERNEL_MX4_GENERAL = 21, /* MX4 codes (mgemm_run_mx4 only): any alignment, VALU, 64x64 tiles */
+    MGEMM_KERNEL_MX4_SKINNY = 22, /* MX4 codes: M <= 64, streams B once, all of K in one workgroup */
+    MGEMM_KERNEL_MX4_MFMA = 23,  /* MX4 codes: 256x256 tiles, block-scaled f8f6f4 MFMA */
+    MGEMM_KERNEL_MX4_MFMA_192 = 24, /* MX4 codes: 256x192 tiles */
+    MGEMM_KERNEL_MX4_MFMA_128 = 25, /* MX4 codes: 128x192 tiles */
+    MGEMM_KERNEL_MX4_MFMA_64 = 26, /* MX4 codes: 64x192 tiles */
+    MGEMM_KERNEL_COUNT = 27
 } mgemm_kernel_t;
 
 /* Output epilogues (see mgemm_run_ex). */
@@ -463,6 +469,89 @@ mgemm_status_t mgemm_run_fp8(mgemm_handle_t h, mgemm_kernel_t kernel, int32_t ks
                              const float* sa, const void* B, int64_t ldb, const float* sb,
                              float beta, void* C, int64_t ldc, mgemm_dtype_t ctype,
                              hipStream_t stream);
+
+/*
+ * Microscaled 4-bit values ("MX4": the MXFP4 format of the OCP Microscaling
+ * Formats specification v1.0).  A row of K values is cut into blocks of 32; a
+ * block is one scale byte b, worth 2^(b - 127) (E8M0; 255 is NaN), and 32
+ * E2M1 codes (sign, 2 exponent bits of bias 1, 1 mantissa bit: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6), two to a byte with the lower k in the low four bits.
+ * A matrix of M rows is two buffers:
+ *   codes  : M rows of 16 * ceil(K/32) bytes, row stride ldq bytes; the codes
+ *            past K in a row's last block are zero;
+ *   scales : M rows of ceil(K/32) bytes, row stride lds bytes.  Every row may
+ *            be read up to its stride, so the buffer holds M * lds bytes.
+ * Code strides and bases that are multiples of 16, and scale strides and
+ * bases that are multiples of 16, take the matrix-core kernels; anything else
+ * is read byte by byte (slow).
+ *
+ * mgemm_quantize_mx4 -- X (M x K, row-major, element type xtype = F32, F16 or
+ * BF16, ldx >= max(1, K)) to codes and scales.  Per block, amax = largest |x|
+ * and e = floor(log2(amax)) - 2, at least -127 (-127 for a block of zeros);
+ * the scale byte is e + 127, and the code of x is the nearest E2M1 value of
+ * x * 2^-e (exact), ties to the even mantissa, magnitudes above 6 to 6, the
+ * sign kept also for zero.  A block with a NaN or an infinity gets scale byte
+ * 255 and codes 0: it stands for NaN throughout.
+ * mgemm_dequantize_mx4 -- the values codes and scales stand for, rounded once
+ * to ytype, into Y (M x K, row-major, ldy >= max(1, K)).
+ * Both: device pointers, asynchronous on `stream`.  M == 0 or K == 0 does
+ * nothing.
+ * Errors: MGEMM_ERR_INVALID_ARG for a NULL handle, negative sizes, a leading
+ * dimension or row stride that is too small, an unknown type or a NULL pointer
+ * with M, K > 0; MGEMM_ERR_UNSUPPORTED for K > 2^33; MGEMM_ERR_HIP.
+ */
+mgemm_status_t mgemm_quantize_mx4(mgemm_handle_t h, int64_t M, int64_t K, const void* X,
+                                  int64_t ldx, mgemm_dtype_t xtype, void* Q, int64_t ldq, void* S,
+                                  int64_t lds, hipStream_t stream);
+mgemm_status_t mgemm_dequantize_mx4(mgemm_handle_t h, int64_t M, int64_t K, const void* Q,
+                                    int64_t ldq, const void* S, int64_t lds, void* Y, int64_t ldy,
+                                    mgemm_dtype_t ytype, hipStream_t stream);
+
+/*
+ * mgemm_run_mx4 -- C = alpha * A B^T + beta * C on MX4 matrices: per output
+ *     C[m][n] = round(alpha * sum_k a[m][k] * b[n][k] + beta * C[m][n])
+ *   A, SA : M rows of codes (stride lda bytes) and scales (stride ldsa);
+ *   B, SB : N rows, one per output column (the weight matrix as out_features
+ *           x in_features; strides ldb, ldsb);
+ *   C     : M x N, row-major, ldc >= max(1, N), type ctype (F32, F16, BF16);
+ *           beta == 0 never reads C.
+ *   kernel, ksplit : as for mgemm_run_fp8, with MGEMM_KERNEL_AUTO or one of
+ *           the MGEMM_KERNEL_MX4_* kernels; K is split into ranges of whole
+ *           128-element slices (MFMA tiles only), the ranges summed in order.
+ * Products of codes and scales are exact; sums are FP32.  A block whose scale
+ * is 255 makes every output of its row or column NaN.
+ * M == 0 or N == 0 does nothing; K == 0 or alpha == 0 gives C = beta * C.
+ * Asynchronous on `stream`.  The split form uses the handle's workspace.
+ * Errors: as mgemm_run_fp8.
+ */
+mgemm_status_t mgemm_run_mx4(mgemm_handle_t h, mgemm_kernel_t kernel, int32_t ksplit, int64_t M,
+                             int64_t N, int64_t K, float alpha, const void* A, int64_t lda,
+                             const void* SA, int64_t ldsa, const void* B, int64_t ldb,
+                             const void* SB, int64_t ldsb, float beta, void* C, int64_t ldc,
+                             mgemm_dtype_t ctype, hipStream_t stream);
+
+/*
+ * mgemm_linear_mx4 -- Y = Q(X) B^T: X (M x K, row-major, type xtype, ldx) is
+ * quantised as mgemm_quantize_mx4 does, within the call, and multiplied as
+ * mgemm_run_mx4 does into Y (M x N, row-major, type ytype, ldy).  Up to 16 rows
+ * are quantised inside the product's own kernel (one launch, X rows 16-byte
+ * aligned); more go through the handle's workspace, a band of rows at a time
+ * where they do not fit, so calls on different streams need different handles.
+ * mgemm_gated_mx4 -- Z = SiLU(Q(X) Bg^T) (.) (Q(X) Bu^T) in the same way,
+ * with both weight matrices N x K and shared strides: per output, with FP32
+ * sums g and u, Z = round(SiLU(g) * u).
+ * Y and Z are written, never read, and must not overlap X.  K == 0 gives
+ * zeros.  Errors: as mgemm_run_mx4; MGEMM_ERR_UNSUPPORTED also when one row's
+ * codes exceed half of the workspace (K > 2^26).
+ */
+mgemm_status_t mgemm_linear_mx4(mgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void* X,
+                                int64_t ldx, mgemm_dtype_t xtype, const void* B, int64_t ldb,
+                                const void* SB, int64_t ldsb, void* Y, int64_t ldy,
+                                mgemm_dtype_t ytype, hipStream_t stream);
+mgemm_status_t mgemm_gated_mx4(mgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void* X,
+                               int64_t ldx, mgemm_dtype_t xtype, const void* Bg, const void* SBg,
+                               const void* Bu, const void* SBu, int64_t ldb, int64_t ldsb, void* Z,
+                               int64_t ldz, mgemm_dtype_t ztype, hipStream_t stream);
 
 /*
  * mgemm_run_noalloc -- mgemm_run_variant without a handle and without any
