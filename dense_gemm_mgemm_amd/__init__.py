@@ -42,7 +42,8 @@ EXPORTED = ["mgemm_create", "mgemm_destroy", "mgemm_run", "mgemm_run_kernel", "m
             "mgemm_status_string",
             "mgemm_kernel_name", "mgemm_num_cu", "mgemm_run_noalloc", "mgemm_set_clock_stamps",
             "mgemm_run_acc32", "mgemm_quantize_mx4", "mgemm_dequantize_mx4", "mgemm_run_mx4",
-            "mgemm_linear_mx4", "mgemm_gated_mx4"]
+            "mgemm_linear_mx4", "mgemm_gated_mx4", "mgemm_gated_workspace",
+            "mgemm_gated_forward", "mgemm_gated_backward"]
 
 
 class MgemmError(RuntimeError):
@@ -119,6 +120,12 @@ def load(path: str | None = None):
                                     ci, vp]
     for name in ("mgemm_quantize_mx4", "mgemm_dequantize_mx4", "mgemm_run_mx4", "mgemm_linear_mx4",
                  "mgemm_gated_mx4"):
+        getattr(lib, name).restype = ci
+    gated = [vp, ci, i64, i64, i64, vp, i64, vp, vp, i64]
+    lib.mgemm_gated_workspace.argtypes = gated[1:] + [ci, ctypes.c_int32, ctypes.c_int32, pi64]
+    lib.mgemm_gated_forward.argtypes = gated + [vp, i64, vp, vp, i64, ci, vp, i64, vp]
+    lib.mgemm_gated_backward.argtypes = gated + [vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, f32, ci, vp, i64, vp]
+    for name in ("mgemm_gated_workspace", "mgemm_gated_forward", "mgemm_gated_backward"):
         getattr(lib, name).restype = ci
     lib.mgemm_status_string.argtypes = [ci]
     lib.mgemm_status_string.restype = ctypes.c_char_p
@@ -396,6 +403,41 @@ def mgemm_gated_mx4(h, M, N, K, X, ldx, xtype, Bg, SBg, Bu, SBu, ldb, ldsb, Z, l
                                 int(ldz), _enum(ztype, _DTYPE), _stream(stream))
     if st != MGEMM_SUCCESS:
         raise MgemmError(st, "mgemm_gated_mx4")
+
+
+def mgemm_gated_workspace(layout, M, N, K, X, ldx, Wg, Wu, ldw, dtype, backward, stored) -> int:
+    """Bytes of workspace that mgemm_gated_forward (backward False) or
+    mgemm_gated_backward needs for these operands (stored: with G and U given)."""
+    out = ctypes.c_int64()
+    st = load().mgemm_gated_workspace(_enum(layout, _LAYOUT), int(M), int(N), int(K), _ptr(X), int(ldx), _ptr(Wg),
+                                      _ptr(Wu), int(ldw), _enum(dtype, _DTYPE), int(bool(backward)),
+                                      int(bool(stored)), ctypes.byref(out))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_gated_workspace")
+    return int(out.value)
+
+
+def mgemm_gated_forward(h, layout, M, N, K, X, ldx, Wg, Wu, ldw, Z, ldz, G, U, ldg, dtype, work, work_bytes,
+                        stream=None) -> None:
+    """Z = SiLU(X Wg) * (X Wu), with G = X Wg and U = X Wu stored unless both
+    are None (weights K x N for layout "row", N x K for "col")."""
+    st = load().mgemm_gated_forward(h, _enum(layout, _LAYOUT), int(M), int(N), int(K), _ptr(X), int(ldx), _ptr(Wg),
+                                    _ptr(Wu), int(ldw), _ptr(Z), int(ldz), _ptr(G), _ptr(U), int(ldg),
+                                    _enum(dtype, _DTYPE), _ptr(work), int(work_bytes), _stream(stream))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_gated_forward")
+
+
+def mgemm_gated_backward(h, layout, M, N, K, X, ldx, Wg, Wu, ldw, G, U, ldg, dZ, lddz, dX, lddx, dWg, dWu, lddw,
+                         beta, dtype, work, work_bytes, stream=None) -> None:
+    """dX (or None), and dWg, dWu = X^T d + beta * dW (or both None), from dZ;
+    G and U as the forward pass stored them, or both None: computed again."""
+    st = load().mgemm_gated_backward(h, _enum(layout, _LAYOUT), int(M), int(N), int(K), _ptr(X), int(ldx), _ptr(Wg),
+                                     _ptr(Wu), int(ldw), _ptr(G), _ptr(U), int(ldg), _ptr(dZ), int(lddz), _ptr(dX),
+                                     int(lddx), _ptr(dWg), _ptr(dWu), int(lddw), float(beta), _enum(dtype, _DTYPE),
+                                     _ptr(work), int(work_bytes), _stream(stream))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_gated_backward")
 
 
 def mgemm_select_kernel(h, layoutA, layoutB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc,

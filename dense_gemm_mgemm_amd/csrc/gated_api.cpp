@@ -1,0 +1,336 @@
+// Entry points of the gated block's training form: argument checks, the
+// workspace's layout, tile and split choice, and the order of launches.  See
+// include/mgemm.h for the contracts.
+#include <hip/hip_runtime.h>
+
+#include "gated.h"
+#include "host.h"
+
+using namespace mgemm_host;
+
+namespace {
+
+using mgemm::BlockArgs;
+using mgemm::BlockForm;
+using mgemm::BlockTile;
+
+constexpr int64_t LIM = (int64_t)1 << 60;
+
+int64_t max1(int64_t x) { return x > 1 ? x : 1; }
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+bool aligned(const void* p) { return ((uintptr_t)p & 15) == 0; }
+mgemm_status_t status(hipError_t e) { return e == hipSuccess ? MGEMM_SUCCESS : MGEMM_ERR_HIP; }
+bool valid_matrix(int64_t rows, int64_t cols, int64_t ld) { return ld >= max1(cols) && (rows == 0 || ld <= LIM / rows); }
+
+// What one call reads, where its copies and gradients lie in the workspace.
+struct Plan {
+    bool col;                         // weights stored out x in
+    int64_t M, N, K;
+    bool copy_x, copy_w;
+    int64_t w_rows, w_cols;           // the stored weights' shape
+    int64_t x_at, wg_at, wu_at;       // byte offsets of the copies
+    int64_t dg_at, du_at, ldd;        // of dG and dU, and their row stride
+    int64_t bytes;                    // the whole workspace, with room to align its start
+};
+
+constexpr int64_t ALIGN = 256;
+
+// The matrix kernels read rows of 16-byte chunks: a stride that is a multiple
+// of 8 and an aligned base, and where a row runs along an output axis (not
+// along the contraction, whose tail is read element by element) a length that
+// is a multiple of 8 as well.  Anything else is copied.
+Plan make_plan(mgemm_layout_t layout, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* Wg,
+               const void* Wu, int64_t ldw, bool forward, bool again, bool dx, bool dw) {
+    Plan p{};
+    p.col = layout == MGEMM_COL_MAJOR;
+    p.M = M; p.N = N; p.K = K;
+    p.w_rows = p.col ? N : K;
+    p.w_cols = p.col ? K : N;
+    const bool uses_x = forward || again || dw, uses_w = forward || again || dx;
+    p.copy_x = uses_x && (ldx % 8 != 0 || !aligned(X) || (dw && K % 8 != 0));
+    const bool w_whole = p.col ? dx && K % 8 != 0 : (forward || again) && N % 8 != 0;
+    p.copy_w = uses_w && (ldw % 8 != 0 || !aligned(Wg) || !aligned(Wu) || w_whole);
+    int64_t at = 0;
+    auto take = [&](int64_t rows, int64_t cols) {
+        const int64_t here = at;
+        at += up(rows * up(cols, 8) * 2, ALIGN);
+        return here;
+    };
+    if (p.copy_x) p.x_at = take(M, K);
+    if (p.copy_w) {
+        p.wg_at = take(p.w_rows, p.w_cols);
+        p.wu_at = take(p.w_rows, p.w_cols);
+    }
+    p.ldd = up(N, 8);
+    if (!forward) {
+        p.dg_at = take(M, N);
+        p.du_at = take(M, N);
+    }
+    p.bytes = at > 0 ? at + ALIGN : 0;
+    return p;
+}
+
+// Tile and split with the smallest predicted time.  The model is that of the
+// 16-bit products: the block's tiles move the same bytes and issue the same
+// matrix instructions per slice.
+BlockTile choose(int num_cu, BlockForm form, const BlockArgs& a, const mgemm::Workspace& ws) {
+    static constexpr BlockTile WIDE[] = {{256, 256, 1}, {256, 192, 1}, {128, 192, 1}};
+    const bool dual = form == mgemm::BLOCK_FORWARD || form == mgemm::BLOCK_AGAIN;
+    const int64_t slices = (a.K / 32) * (form == mgemm::BLOCK_DX ? 2 : 1);
+    BlockTile best{0, 0, 0};
+    double best_t = 1e300;
+    for (const BlockTile& c : WIDE) {
+        if (dual && c.bn != 192) continue;
+        const int out = dual ? 96 : c.bn;
+        Problem q{};
+        q.M = up(a.M, c.bm) * a.batches_m;
+        q.N = up(a.N, out) * a.batches_n;
+        q.K = a.K * (form == mgemm::BLOCK_DX ? 2 : 1);
+        q.num_cu = num_cu;
+        for (int req = 1, last = 0; req <= mgemm::MAX_KSPLIT; ++req) {
+            const BlockTile t{c.bm, c.bn, mgemm::block_splits(slices, req)};
+            if (t.ks <= last) continue;
+            last = t.ks;
+            if (t.ks > 1 && mgemm::block_part_bytes(form, a, t) > ws.part_bytes) break;
+            const double us = predict_us(q, c.bm, c.bn, out, c.bn == 256 ? 1.4 : 1.3, 1, t.ks);
+            if (us < best_t) { best_t = us; best = t; }
+        }
+    }
+    return best;
+}
+
+// Whether the grids and slice counts of these sizes stay within 32 bits.
+bool fits(int64_t M, int64_t N, int64_t K) {
+    const int64_t most = (int64_t)0x7fffffff / 64;
+    auto tiles = [](int64_t m, int64_t n) { return ((m + 127) / 128) * 2 * ((n + 95) / 96); };
+    return M / 32 < 0x3fffffff && N / 32 < 0x3fffffff && K / 32 < 0x3fffffff && (M + 127) / 128 < most &&
+           (N + 95) / 96 < most && (K + 95) / 96 < most && tiles(M, N) < most && tiles(M, K) < most &&
+           tiles(K, N) < most && tiles(N, K) < most;
+}
+
+BlockArgs base_args(const mgemm::Workspace& ws) {
+    BlockArgs a{};
+    a.batches_m = a.batches_n = 1;
+    a.part = (float*)ws.part;
+    return a;
+}
+
+struct Operands {
+    const void *X, *Wg, *Wu;
+    int64_t ldx, ldw;
+};
+
+// Copies what has to be copied, and says where the operands are from then on.
+mgemm_status_t lay_out(const Plan& p, char* work, Operands& o, hipStream_t s) {
+    mgemm::Repack r{};
+    auto add = [&](const void*& src, int64_t rows, int64_t cols, int64_t ld, int64_t at) {
+        r.src[r.n] = src;
+        r.dst[r.n] = work + at;
+        r.rows[r.n] = rows; r.cols[r.n] = cols; r.lds[r.n] = ld; r.ldd[r.n] = up(cols, 8);
+        ++r.n;
+        src = work + at;
+    };
+    if (p.copy_x) {
+        add(o.X, p.M, p.K, o.ldx, p.x_at);
+        o.ldx = up(p.K, 8);
+    }
+    if (p.copy_w) {
+        add(o.Wg, p.w_rows, p.w_cols, o.ldw, p.wg_at);
+        add(o.Wu, p.w_rows, p.w_cols, o.ldw, p.wu_at);
+        o.ldw = up(p.w_cols, 8);
+    }
+    return r.n > 0 ? status(mgemm::launch_repack(r, s)) : MGEMM_SUCCESS;
+}
+
+// C (rows x cols, 16-bit) = beta * C.
+mgemm_status_t scale(mgemm_handle_t h, void* C, int64_t rows, int64_t cols, int64_t ld, float beta, int dtype,
+                     hipStream_t s) {
+    if (C == nullptr || rows == 0 || cols == 0) return MGEMM_SUCCESS;
+    Problem q{};
+    q.M = rows; q.N = cols;
+    q.beta = beta;
+    q.C = C; q.ldc = ld;
+    q.dtype = dtype;
+    q.num_cu = h->num_cu;
+    q.epilogue = mgemm::EPI_NONE;
+    return status(mgemm::launch_scale(q, s));
+}
+
+mgemm_status_t check_common(mgemm_layout_t layout, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw,
+                            mgemm_dtype_t dtype) {
+    if (layout != MGEMM_ROW_MAJOR && layout != MGEMM_COL_MAJOR) return MGEMM_ERR_INVALID_ARG;
+    if (dtype != MGEMM_F32 && dtype != MGEMM_F16 && dtype != MGEMM_BF16) return MGEMM_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0 || M > LIM || N > LIM || K > LIM) return MGEMM_ERR_INVALID_ARG;
+    const bool col = layout == MGEMM_COL_MAJOR;
+    if (!valid_matrix(M, K, ldx) || !valid_matrix(col ? N : K, col ? K : N, ldw)) return MGEMM_ERR_INVALID_ARG;
+    if (dtype == MGEMM_F32) return MGEMM_ERR_UNSUPPORTED;
+    // The workspace's byte counts are sums of a few products of two sizes.
+    const int64_t lim = LIM / 8;
+    if ((N > 0 && M > lim / (N + 8)) || (K > 0 && M > lim / (K + 8)) || (K > 0 && N > lim / (K + 8)) ||
+        (N > 0 && K > lim / (N + 8)))
+        return MGEMM_ERR_INVALID_ARG;
+    return MGEMM_SUCCESS;
+}
+
+// The workspace's start (aligned), or null when it is too small.
+mgemm_status_t check_work(const Plan& p, void* work, int64_t bytes, char** out) {
+    *out = nullptr;
+    if (p.bytes == 0) return MGEMM_SUCCESS;
+    if (work == nullptr || bytes < p.bytes) return MGEMM_ERR_INVALID_ARG;
+    *out = (char*)up((int64_t)(uintptr_t)work, ALIGN);
+    return MGEMM_SUCCESS;
+}
+
+}  // namespace
+
+namespace mgemm {
+
+int block_splits(int64_t slices, int requested) {
+    if (requested <= 1 || slices < 2) return 1;
+    const int64_t ks = requested < slices ? requested : slices, nks = (slices + ks - 1) / ks;
+    return (int)((slices + nks - 1) / nks);
+}
+
+int64_t block_tiles(BlockForm f, const BlockArgs& a, BlockTile t) {
+    const int out = f == BLOCK_FORWARD || f == BLOCK_AGAIN ? 96 : t.bn;
+    return (a.M + t.bm - 1) / t.bm * a.batches_m * ((a.N + out - 1) / out * a.batches_n);
+}
+
+int64_t block_part_bytes(BlockForm f, const BlockArgs& a, BlockTile t) {
+    return block_tiles(f, a, t) * t.ks * t.bm * t.bn * 4;
+}
+
+}  // namespace mgemm
+
+extern "C" {
+
+mgemm_status_t mgemm_gated_workspace(mgemm_layout_t layoutW, int64_t M, int64_t N, int64_t K, const void* X,
+                                     int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, mgemm_dtype_t dtype,
+                                     int32_t backward, int32_t stored, int64_t* bytes) {
+    if (!bytes) return MGEMM_ERR_INVALID_ARG;
+    const mgemm_status_t st = check_common(layoutW, M, N, K, ldx, ldw, dtype);
+    if (st != MGEMM_SUCCESS) return st;
+    const bool b = backward != 0;
+    *bytes = M == 0 || N == 0 || K == 0
+                 ? 0
+                 : make_plan(layoutW, M, N, K, X, ldx, Wg, Wu, ldw, !b, b && stored == 0, b, b).bytes;
+    return MGEMM_SUCCESS;
+}
+
+mgemm_status_t mgemm_gated_forward(mgemm_handle_t h, mgemm_layout_t layoutW, int64_t M, int64_t N, int64_t K,
+                                   const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, void* Z,
+                                   int64_t ldz, void* G, void* U, int64_t ldg, mgemm_dtype_t dtype, void* work,
+                                   int64_t work_bytes, hipStream_t stream) {
+    if (!h) return MGEMM_ERR_INVALID_ARG;
+    if (const mgemm_status_t st = check_common(layoutW, M, N, K, ldx, ldw, dtype); st != MGEMM_SUCCESS) return st;
+    if (!valid_matrix(M, N, ldz) || (G == nullptr) != (U == nullptr) || (G && !valid_matrix(M, N, ldg)))
+        return MGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return MGEMM_SUCCESS;
+    if (!Z) return MGEMM_ERR_INVALID_ARG;
+    if (K == 0) {                                     // G = U = Z = 0
+        mgemm_status_t st = scale(h, Z, M, N, ldz, 0.0f, (int)dtype, stream);
+        if (st == MGEMM_SUCCESS) st = scale(h, G, M, N, ldg, 0.0f, (int)dtype, stream);
+        if (st == MGEMM_SUCCESS) st = scale(h, U, M, N, ldg, 0.0f, (int)dtype, stream);
+        return st;
+    }
+    if (!X || !Wg || !Wu) return MGEMM_ERR_INVALID_ARG;
+    if (!fits(M, N, K)) return MGEMM_ERR_UNSUPPORTED;
+    const Plan p = make_plan(layoutW, M, N, K, X, ldx, Wg, Wu, ldw, true, false, false, false);
+    char* w;
+    if (const mgemm_status_t st = check_work(p, work, work_bytes, &w); st != MGEMM_SUCCESS) return st;
+    Operands o{X, Wg, Wu, ldx, ldw};
+    if (const mgemm_status_t st = lay_out(p, w, o, stream); st != MGEMM_SUCCESS) return st;
+    BlockArgs a = base_args(h->ws);
+    a.M = M; a.N = N; a.K = K;
+    a.A[0] = a.A[1] = o.X; a.lda = o.ldx;
+    a.B[0] = o.Wg; a.B[1] = o.Wu; a.ldb = o.ldw;
+    a.Mr = up(M, 8); a.Nr = up(N, 8);
+    a.Z = Z; a.ldz = ldz;
+    a.C[0] = G; a.C[1] = U; a.ldc = ldg;
+    return status(mgemm::launch_block_forward(a, (int)dtype, p.col, false,
+                                              choose(h->num_cu, mgemm::BLOCK_FORWARD, a, h->ws), stream));
+}
+
+mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, int64_t M, int64_t N, int64_t K,
+                                    const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw,
+                                    const void* G, const void* U, int64_t ldg, const void* dZ, int64_t lddz, void* dX,
+                                    int64_t lddx, void* dWg, void* dWu, int64_t lddw, float beta, mgemm_dtype_t dtype,
+                                    void* work, int64_t work_bytes, hipStream_t stream) {
+    if (!h) return MGEMM_ERR_INVALID_ARG;
+    if (const mgemm_status_t st = check_common(layoutW, M, N, K, ldx, ldw, dtype); st != MGEMM_SUCCESS) return st;
+    const bool col = layoutW == MGEMM_COL_MAJOR, again = G == nullptr;
+    if ((G == nullptr) != (U == nullptr) || (dWg == nullptr) != (dWu == nullptr)) return MGEMM_ERR_INVALID_ARG;
+    if (!valid_matrix(M, N, lddz) || (G && !valid_matrix(M, N, ldg)) || (dX && !valid_matrix(M, K, lddx)) ||
+        (dWg && !valid_matrix(col ? N : K, col ? K : N, lddw)))
+        return MGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0 || K == 0) {                 // no terms: dX = 0, dW = beta * dW
+        const int64_t rows = col ? N : K, cols = col ? K : N;
+        mgemm_status_t st = scale(h, dX, M, K, lddx, 0.0f, (int)dtype, stream);
+        if (st == MGEMM_SUCCESS) st = scale(h, dWg, rows, cols, lddw, beta, (int)dtype, stream);
+        if (st == MGEMM_SUCCESS) st = scale(h, dWu, rows, cols, lddw, beta, (int)dtype, stream);
+        return st;
+    }
+    if (!dX && !dWg) return MGEMM_SUCCESS;
+    if (!dZ || ((again || dWg) && !X) || ((again || dX) && (!Wg || !Wu))) return MGEMM_ERR_INVALID_ARG;
+    if (!fits(M, N, K)) return MGEMM_ERR_UNSUPPORTED;
+    const Plan p = make_plan(layoutW, M, N, K, X, ldx, Wg, Wu, ldw, false, again, dX != nullptr, dWg != nullptr);
+    char* w;
+    if (const mgemm_status_t st = check_work(p, work, work_bytes, &w); st != MGEMM_SUCCESS) return st;
+    Operands o{X, Wg, Wu, ldx, ldw};
+    if (const mgemm_status_t st = lay_out(p, w, o, stream); st != MGEMM_SUCCESS) return st;
+    void *dG = w + p.dg_at, *dU = w + p.du_at;
+
+    if (again) {
+        BlockArgs a = base_args(h->ws);
+        a.M = M; a.N = N; a.K = K;
+        a.A[0] = a.A[1] = o.X; a.lda = o.ldx;
+        a.B[0] = o.Wg; a.B[1] = o.Wu; a.ldb = o.ldw;
+        a.Mr = up(M, 8); a.Nr = up(N, 8);
+        a.dZ = dZ; a.ldz = lddz;
+        a.C[0] = dG; a.C[1] = dU; a.ldc = p.ldd;
+        if (hipError_t e = mgemm::launch_block_forward(a, (int)dtype, col, true,
+                                                       choose(h->num_cu, mgemm::BLOCK_AGAIN, a, h->ws), stream);
+            e != hipSuccess)
+            return MGEMM_ERR_HIP;
+    } else if (hipError_t e = mgemm::launch_gated_grad(M, N, G, U, ldg, dZ, lddz, dG, dU, p.ldd, (int)dtype, stream);
+               e != hipSuccess) {
+        return MGEMM_ERR_HIP;
+    }
+    if (dX) {
+        BlockArgs a = base_args(h->ws);
+        a.M = M; a.N = K; a.K = N;
+        a.A[0] = dG; a.A[1] = dU; a.lda = p.ldd;
+        a.B[0] = o.Wg; a.B[1] = o.Wu; a.ldb = o.ldw;
+        a.Mr = up(M, 8); a.Nr = up(K, 8);
+        a.C[0] = a.C[1] = dX; a.ldc = lddx;
+        // Row-major weights (in x out) are contiguous along this contraction.
+        if (hipError_t e = mgemm::launch_block_dx(a, (int)dtype, !col, choose(h->num_cu, mgemm::BLOCK_DX, a, h->ws),
+                                                  stream);
+            e != hipSuccess)
+            return MGEMM_ERR_HIP;
+    }
+    if (dWg) {
+        BlockArgs a = base_args(h->ws);
+        a.K = M;
+        a.beta = beta;
+        a.C[0] = dWg; a.C[1] = dWu; a.ldc = lddw;
+        if (col) {
+            a.M = N; a.N = K;
+            a.A[0] = dG; a.A[1] = dU; a.lda = p.ldd;
+            a.B[0] = a.B[1] = o.X; a.ldb = o.ldx;
+            a.batches_m = 2;
+        } else {
+            a.M = K; a.N = N;
+            a.A[0] = a.A[1] = o.X; a.lda = o.ldx;
+            a.B[0] = dG; a.B[1] = dU; a.ldb = p.ldd;
+            a.batches_n = 2;
+        }
+        a.Mr = up(a.M, 8); a.Nr = up(a.N, 8);
+        if (hipError_t e = mgemm::launch_block_dw(a, (int)dtype, choose(h->num_cu, mgemm::BLOCK_DW, a, h->ws), stream);
+            e != hipSuccess)
+            return MGEMM_ERR_HIP;
+    }
+    return MGEMM_SUCCESS;
+}
+
+}  // extern "C"

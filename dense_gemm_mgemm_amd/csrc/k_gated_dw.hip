@@ -1,0 +1,21 @@
+// dWg = X^T dG and dWu = X^T dU (or their transposes) in one grid (see
+// gated_tile.h): A is contiguous along the outputs' rows, B along their columns.
+#include "gated_tile.h"
+
+namespace mgemm {
+namespace {
+
+template <int DT>
+hipError_t by_tile(const BlockArgs& a, BlockTile t, hipStream_t s) {
+    if (t.bm == 128) return launch_block<DT, BLOCK_DW, 128, 192, true, false>(a, t.ks, s);
+    if (t.bn == 192) return launch_block<DT, BLOCK_DW, 256, 192, true, false>(a, t.ks, s);
+    return launch_block<DT, BLOCK_DW, 256, 256, true, false>(a, t.ks, s);
+}
+
+}  // namespace
+
+hipError_t launch_block_dw(const BlockArgs& a, int dtype, BlockTile t, hipStream_t s) {
+    return dtype == F16 ? by_tile<F16>(a, t, s) : by_tile<BF16>(a, t, s);
+}
+
+}  // namespace mgemm

@@ -1,0 +1,21 @@
+// dX = dG Wg^T + dU Wu^T as one product over two segments (see gated_tile.h).
+#include "gated_tile.h"
+
+namespace mgemm {
+namespace {
+
+template <int DT, bool BKC>
+hipError_t by_tile(const BlockArgs& a, BlockTile t, hipStream_t s) {
+    if (t.bm == 128) return launch_block<DT, BLOCK_DX, 128, 192, false, BKC>(a, t.ks, s);
+    if (t.bn == 192) return launch_block<DT, BLOCK_DX, 256, 192, false, BKC>(a, t.ks, s);
+    return launch_block<DT, BLOCK_DX, 256, 256, false, BKC>(a, t.ks, s);
+}
+
+}  // namespace
+
+hipError_t launch_block_dx(const BlockArgs& a, int dtype, bool b_kc, BlockTile t, hipStream_t s) {
+    if (dtype == F16) return b_kc ? by_tile<F16, true>(a, t, s) : by_tile<F16, false>(a, t, s);
+    return b_kc ? by_tile<BF16, true>(a, t, s) : by_tile<BF16, false>(a, t, s);
+}
+
+}  // namespace mgemm

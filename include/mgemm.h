@@ -554,6 +554,66 @@ mgemm_status_t mgemm_gated_mx4(mgemm_handle_t h, int64_t M, int64_t N, int64_t K
                                int64_t ldz, mgemm_dtype_t ztype, hipStream_t stream);
 
 /*
+ * Training form of the gated block, FP16 and BF16: with X (M x K, row-major)
+ * and two weights Wg and Wu,
+ *     G = X Wg,  U = X Wu,  Z = SiLU(G) (.) U                       (forward)
+ *     s = 1 / (1 + e^-G),  dU = dZ (.) G s,
+ *     dG = dZ (.) U s (1 + G (1 - s)),
+ *     dX = dG Wg^T + dU Wu^T,  dWg = X^T dG,  dWu = X^T dU         (backward)
+ *   layoutW : MGEMM_ROW_MAJOR: the weights (and their gradients) are K x N,
+ *        ldw >= max(1, N); MGEMM_COL_MAJOR: they are stored out x in, N x K
+ *        with ldw >= max(1, K).
+ *   work : device workspace of mgemm_gated_workspace's bytes for the same
+ *        arguments (any alignment; NULL where that is 0).  Calls that may run at
+ *        the same time need different workspaces and different handles.
+ * All matrices are row-major with leading dimensions in elements; G and U
+ * share one (ldg), as do both weights (ldw) and both gradients (lddw).  Any
+ * sizes, strides and alignments: operands that the matrix kernels cannot read
+ * in place (rows that are not 16-byte aligned, or a length that is not a
+ * multiple of 8 along an output axis) are copied into the workspace first.
+ * FP32 sums; each output is rounded once.  Outputs must not overlap inputs.
+ * A fixed problem gives the same bits on every run.  Asynchronous on `stream`.
+ *
+ * mgemm_gated_workspace -- bytes that a call needs: `backward` 0 for
+ * mgemm_gated_forward, else mgemm_gated_backward with (`stored` != 0) or
+ * without G and U.  The pointers are only inspected for their alignment.
+ *
+ * mgemm_gated_forward -- Z and, unless both are NULL, G and U, each rounded
+ * once from the FP32 sums.  K == 0 gives zeros.
+ *
+ * mgemm_gated_backward -- from dZ (M x N) the gradients
+ *   dX  : M x K, written, never read (NULL: not computed);
+ *   dWg, dWu : dW = X^T d + beta * dW in the weights' layout; beta == 0 never
+ *        reads them (both NULL: not computed).
+ * G and U are the forward pass's stored matrices, or both NULL: they are
+ * computed again, rounded as the forward pass would have stored them.  dG and
+ * dU are rounded to dtype between the two stages, as the operands of the
+ * products have to be.  M == 0 or N == 0: dX = 0 and dW = beta * dW.
+ *
+ * Errors: MGEMM_ERR_INVALID_ARG for negative sizes, an unknown layout or type,
+ * a leading dimension that is too small, one of a pair NULL without the other,
+ * a NULL pointer that is needed, or a workspace that is too small (nothing
+ * enqueued); MGEMM_ERR_UNSUPPORTED for MGEMM_F32 or grids past 32 bits;
+ * MGEMM_ERR_HIP for a failed launch.
+ */
+mgemm_status_t mgemm_gated_workspace(mgemm_layout_t layoutW, int64_t M, int64_t N, int64_t K,
+                                     const void* X, int64_t ldx, const void* Wg, const void* Wu,
+                                     int64_t ldw, mgemm_dtype_t dtype, int32_t backward,
+                                     int32_t stored, int64_t* bytes);
+mgemm_status_t mgemm_gated_forward(mgemm_handle_t h, mgemm_layout_t layoutW, int64_t M, int64_t N,
+                                   int64_t K, const void* X, int64_t ldx, const void* Wg,
+                                   const void* Wu, int64_t ldw, void* Z, int64_t ldz, void* G,
+                                   void* U, int64_t ldg, mgemm_dtype_t dtype, void* work,
+                                   int64_t work_bytes, hipStream_t stream);
+mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, int64_t M, int64_t N,
+                                    int64_t K, const void* X, int64_t ldx, const void* Wg,
+                                    const void* Wu, int64_t ldw, const void* G, const void* U,
+                                    int64_t ldg, const void* dZ, int64_t lddz, void* dX,
+                                    int64_t lddx, void* dWg, void* dWu, int64_t lddw, float beta,
+                                    mgemm_dtype_t dtype, void* work, int64_t work_bytes,
+                                    hipStream_t stream);
+
+/*
  * mgemm_run_noalloc -- mgemm_run_variant without a handle and without any
  * device allocation, for callers that cannot allocate: code being captured
  * into a HIP graph, tight serving loops, harnesses that forbid hipMalloc.
