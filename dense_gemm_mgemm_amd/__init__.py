@@ -43,7 +43,7 @@ EXPORTED = ["mgemm_create", "mgemm_destroy", "mgemm_run", "mgemm_run_kernel", "m
             "mgemm_kernel_name", "mgemm_num_cu", "mgemm_run_noalloc", "mgemm_set_clock_stamps",
             "mgemm_run_acc32", "mgemm_quantize_mx4", "mgemm_dequantize_mx4", "mgemm_run_mx4",
             "mgemm_linear_mx4", "mgemm_gated_mx4", "mgemm_gated_workspace",
-            "mgemm_gated_forward", "mgemm_gated_backward"]
+            "mgemm_gated_forward", "mgemm_gated_backward", "mgemm_set_gated_tile"]
 
 
 class MgemmError(RuntimeError):
@@ -125,7 +125,8 @@ def load(path: str | None = None):
     lib.mgemm_gated_workspace.argtypes = gated[1:] + [ci, ctypes.c_int32, ctypes.c_int32, pi64]
     lib.mgemm_gated_forward.argtypes = gated + [vp, i64, vp, vp, i64, ci, vp, i64, vp]
     lib.mgemm_gated_backward.argtypes = gated + [vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, f32, ci, vp, i64, vp]
-    for name in ("mgemm_gated_workspace", "mgemm_gated_forward", "mgemm_gated_backward"):
+    lib.mgemm_set_gated_tile.argtypes = [vp] + [ctypes.c_int32] * 4
+    for name in ("mgemm_gated_workspace", "mgemm_gated_forward", "mgemm_gated_backward", "mgemm_set_gated_tile"):
         getattr(lib, name).restype = ci
     lib.mgemm_status_string.argtypes = [ci]
     lib.mgemm_status_string.restype = ctypes.c_char_p
@@ -438,6 +439,14 @@ def mgemm_gated_backward(h, layout, M, N, K, X, ldx, Wg, Wu, ldw, G, U, ldg, dZ,
                                      _ptr(work), int(work_bytes), _stream(stream))
     if st != MGEMM_SUCCESS:
         raise MgemmError(st, "mgemm_gated_backward")
+
+
+def mgemm_set_gated_tile(h, product, rows=0, columns=0, ksplit=0) -> None:
+    """Check hook: forces the tile of a product of the gated block (0 the forward
+    pair, 1 dX, 2 the weights' gradients); rows 0: the library's choice."""
+    st = load().mgemm_set_gated_tile(h, int(product), int(rows), int(columns), int(ksplit))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_set_gated_tile")
 
 
 def mgemm_select_kernel(h, layoutA, layoutB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc,

@@ -21,11 +21,12 @@ struct BlockArgs {
     int64_t ldc;
     int batches_m, batches_n; // weights' gradients: 2 along the axis whose operand differs, else 1
     float beta;
-    const void* dZ;           // recomputed backward
+    const void* dZ;           // recomputed backward: Mz x Nz, zeros beyond
+    int64_t Mz, Nz;
     void* Z;                  // forward
     int64_t ldz;              // of Z or dZ
     float* part;              // split contraction: [tile][range][chunk][thread] f32x4
-    int ksplit, nks;          // ranges, and 32-element slices per range
+    int ksplit, nks;          // ranges, and slices per range
 };
 
 // Which product: the pair G, U with its epilogue, dX (two segments summed),
@@ -33,10 +34,14 @@ struct BlockArgs {
 enum BlockForm : int { BLOCK_FORWARD = 0, BLOCK_AGAIN = 1, BLOCK_DX = 2, BLOCK_DW = 3 };
 
 struct BlockTile {
-    int bm, bn;               // rows and B columns of a tile (forward: 96 outputs of each product)
+    int bm, bn;               // rows and B columns of a tile (forward: bn / 2 outputs of each product)
     int ks;                   // ranges of the contraction
 };
 
+// Elements of the contraction that a tile of bm rows takes per slice.
+constexpr int slice_of(int bm) { return bm == 256 ? 32 : 64; }
+// Whether a product has a tile of this size.
+bool block_has(BlockForm f, int bm, int bn);
 // Ranges that a request for at most `requested` turns into (whole slices per range).
 int block_splits(int64_t slices, int requested);
 // Bytes of the partial sums of a split launch.
@@ -49,14 +54,21 @@ hipError_t launch_block_forward(const BlockArgs& a, int dtype, bool b_kc, bool a
 hipError_t launch_block_dx(const BlockArgs& a, int dtype, bool b_kc, BlockTile t, hipStream_t s);
 hipError_t launch_block_dw(const BlockArgs& a, int dtype, BlockTile t, hipStream_t s);
 
-// dG and dU (row stride ldd, a multiple of 8, 16-byte aligned) from G, U and dZ.
-hipError_t launch_gated_grad(int64_t M, int64_t N, const void* G, const void* U, int64_t ldg, const void* dZ,
+// dX and the weights' gradients in one launch, both in 128x128 tiles, and
+// one more for the sums of what is split.
+hipError_t launch_block_pair(const BlockArgs& x, const BlockArgs& w, int dtype, bool b_kc, int xks, int wks,
+                             hipStream_t s);
+
+// dG and dU from G, U and dZ (M x N): Mo x No of them, zeros past M x N, in
+// rows of ldd elements (No and ldd multiples of 8, 16-byte aligned).
+hipError_t launch_gated_grad(int64_t M, int64_t N, int64_t Mo, int64_t No, const void* G, const void* U, int64_t ldg, const void* dZ,
                              int64_t lddz, void* dG, void* dU, int64_t ldd, int dtype, hipStream_t s);
-// Copies up to three 16-bit matrices to rows of a multiple of 8 elements (16-byte aligned).
+// Copies up to three 16-bit matrices to rows of ldd elements (a multiple of 8,
+// 16-byte aligned), zeros past their columns and in the rows up to rows_out.
 struct Repack {
     const void* src[3];
     void* dst[3];
-    int64_t rows[3], cols[3], lds[3], ldd[3];
+    int64_t rows[3], cols[3], lds[3], ldd[3], rows_out[3];
     int n;
 };
 hipError_t launch_repack(const Repack& r, hipStream_t s);

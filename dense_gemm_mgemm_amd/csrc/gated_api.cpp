@@ -29,11 +29,17 @@ struct Plan {
     bool copy_x, copy_w;
     int64_t w_rows, w_cols;           // the stored weights' shape
     int64_t x_at, wg_at, wu_at;       // byte offsets of the copies
-    int64_t dg_at, du_at, ldd;        // of dG and dU, and their row stride
+    int64_t dg_at, du_at;             // of dG and dU,
+    int64_t d_rows, d_cols;           //   d_rows x d_cols each, packed
     int64_t bytes;                    // the whole workspace, with room to align its start
 };
 
 constexpr int64_t ALIGN = 256;
+// Copies are padded with zeros to whole slices of the matrix kernels, and dG
+// and dU along an axis that meets a copy: a contraction of two padded operands
+// runs over the padded length and has no tail, which costs a workgroup 1.5 to
+// 3 us (ordinary loads that nothing overlaps).
+constexpr int64_t SLICE = 64;
 
 // The matrix kernels read rows of 16-byte chunks: a stride that is a multiple
 // of 8 and an aligned base, and where a row runs along an output axis (not
@@ -53,18 +59,19 @@ Plan make_plan(mgemm_layout_t layout, int64_t M, int64_t N, int64_t K, const voi
     int64_t at = 0;
     auto take = [&](int64_t rows, int64_t cols) {
         const int64_t here = at;
-        at += up(rows * up(cols, 8) * 2, ALIGN);
+        at += up(rows * cols * 2, ALIGN);
         return here;
     };
-    if (p.copy_x) p.x_at = take(M, K);
+    if (p.copy_x) p.x_at = take(up(M, SLICE), up(K, SLICE));
     if (p.copy_w) {
-        p.wg_at = take(p.w_rows, p.w_cols);
-        p.wu_at = take(p.w_rows, p.w_cols);
+        p.wg_at = take(up(p.w_rows, SLICE), up(p.w_cols, SLICE));
+        p.wu_at = take(up(p.w_rows, SLICE), up(p.w_cols, SLICE));
     }
-    p.ldd = up(N, 8);
+    p.d_rows = p.copy_x ? up(M, SLICE) : M;
+    p.d_cols = up(N, p.copy_w ? SLICE : 8);
     if (!forward) {
-        p.dg_at = take(M, N);
-        p.du_at = take(M, N);
+        p.dg_at = take(p.d_rows, p.d_cols);
+        p.du_at = take(p.d_rows, p.d_cols);
     }
     p.bytes = at > 0 ? at + ALIGN : 0;
     return p;
@@ -73,43 +80,64 @@ Plan make_plan(mgemm_layout_t layout, int64_t M, int64_t N, int64_t K, const voi
 // Tile and split with the smallest predicted time.  The model is that of the
 // 16-bit products: the block's tiles move the same bytes and issue the same
 // matrix instructions per slice.
-BlockTile choose(int num_cu, BlockForm form, const BlockArgs& a, const mgemm::Workspace& ws) {
-    static constexpr BlockTile WIDE[] = {{256, 256, 1}, {256, 192, 1}, {128, 192, 1}};
+BlockTile choose(mgemm_handle_t h, BlockForm form, const BlockArgs& a) {
     const bool dual = form == mgemm::BLOCK_FORWARD || form == mgemm::BLOCK_AGAIN;
-    const int64_t slices = (a.K / 32) * (form == mgemm::BLOCK_DX ? 2 : 1);
+    const mgemm_host::GatedTile& forced = h->gated_tile[dual ? 0 : form == mgemm::BLOCK_DX ? 1 : 2];
     BlockTile best{0, 0, 0};
     double best_t = 1e300;
-    for (const BlockTile& c : WIDE) {
-        if (dual && c.bn != 192) continue;
-        const int out = dual ? 96 : c.bn;
-        Problem q{};
-        q.M = up(a.M, c.bm) * a.batches_m;
-        q.N = up(a.N, out) * a.batches_n;
-        q.K = a.K * (form == mgemm::BLOCK_DX ? 2 : 1);
-        q.num_cu = num_cu;
-        for (int req = 1, last = 0; req <= mgemm::MAX_KSPLIT; ++req) {
-            const BlockTile t{c.bm, c.bn, mgemm::block_splits(slices, req)};
-            if (t.ks <= last) continue;
-            last = t.ks;
-            if (t.ks > 1 && mgemm::block_part_bytes(form, a, t) > ws.part_bytes) break;
-            const double us = predict_us(q, c.bm, c.bn, out, c.bn == 256 ? 1.4 : 1.3, 1, t.ks);
-            if (us < best_t) { best_t = us; best = t; }
+    for (int bm : {256, 128})
+        for (int bn : {256, 192, 128}) {
+            if (!mgemm::block_has(form, bm, bn)) continue;
+            if (forced.rows != 0 && (forced.rows != bm || forced.columns != bn)) continue;
+            const int out = dual ? bn / 2 : bn;
+            const int64_t slices = a.K / mgemm::slice_of(bm) * (form == mgemm::BLOCK_DX ? 2 : 1);
+            Problem q{};
+            q.M = up(a.M, bm) * a.batches_m;
+            q.N = up(a.N, out) * a.batches_n;
+            q.K = a.K * (form == mgemm::BLOCK_DX ? 2 : 1);
+            q.num_cu = h->num_cu;
+            for (int req = 1, last = 0; req <= mgemm::MAX_KSPLIT; ++req) {
+                if (forced.rows != 0 && forced.ksplit != 0 && req != forced.ksplit) continue;
+                const BlockTile t{bm, bn, mgemm::block_splits(slices, req)};
+                if (t.ks <= last) continue;
+                last = t.ks;
+                if (t.ks > 1 && mgemm::block_part_bytes(form, a, t) > h->ws.part_bytes) break;
+                const double us = predict_us(q, bm, bn, out, bn == 256 ? 1.4 : 1.3, 1, t.ks);
+                if (us < best_t) { best_t = us; best = t; }
+            }
         }
-    }
     return best;
+}
+
+// Whether dX and the weights' gradients run as one launch of 128x128 tiles;
+// then xt and wt become its splits.
+bool choose_pair(mgemm_handle_t h, const BlockArgs& x, const BlockArgs& w, BlockTile& xt, BlockTile& wt) {
+    const auto &fx = h->gated_tile[1], &fw = h->gated_tile[2];
+    const int64_t cus = h->num_cu > 0 ? h->num_cu : 256;
+    const BlockTile one{128, 128, 1};
+    const int64_t nx = mgemm::block_tiles(mgemm::BLOCK_DX, x, one), nw = mgemm::block_tiles(mgemm::BLOCK_DW, w, one);
+    auto small = [](const BlockTile& t) { return t.bm == 128 && t.bn == 128; };
+    if (fx.rows != 0 || fw.rows != 0)
+        return small(xt) && small(wt) && nx * xt.ks + nw * wt.ks <= 2 * cus &&
+               mgemm::block_part_bytes(mgemm::BLOCK_DX, x, xt) + mgemm::block_part_bytes(mgemm::BLOCK_DW, w, wt) <=
+                   h->ws.part_bytes;
+    return small(xt) && small(wt) && nx + nw <= cus && xt.ks == 1 && wt.ks == 1;
 }
 
 // Whether the grids and slice counts of these sizes stay within 32 bits.
 bool fits(int64_t M, int64_t N, int64_t K) {
     const int64_t most = (int64_t)0x7fffffff / 64;
-    auto tiles = [](int64_t m, int64_t n) { return ((m + 127) / 128) * 2 * ((n + 95) / 96); };
+    auto tiles = [](int64_t m, int64_t n) { return ((m + 127) / 128) * 2 * ((n + 63) / 64); };
     return M / 32 < 0x3fffffff && N / 32 < 0x3fffffff && K / 32 < 0x3fffffff && (M + 127) / 128 < most &&
-           (N + 95) / 96 < most && (K + 95) / 96 < most && tiles(M, N) < most && tiles(M, K) < most &&
+           (N + 63) / 64 < most && (K + 63) / 64 < most && tiles(M, N) < most && tiles(M, K) < most &&
            tiles(K, N) < most && tiles(N, K) < most;
 }
 
-BlockArgs base_args(const mgemm::Workspace& ws) {
+// Outputs M x N (two of them along an axis with two batches) of a contraction over K.
+BlockArgs base_args(const mgemm::Workspace& ws, int64_t M, int64_t N, int64_t K) {
     BlockArgs a{};
+    a.M = M; a.N = N; a.K = K;
+    a.Mr = up(M, 8); a.Nr = up(N, 8);
     a.batches_m = a.batches_n = 1;
     a.part = (float*)ws.part;
     return a;
@@ -126,18 +154,19 @@ mgemm_status_t lay_out(const Plan& p, char* work, Operands& o, hipStream_t s) {
     auto add = [&](const void*& src, int64_t rows, int64_t cols, int64_t ld, int64_t at) {
         r.src[r.n] = src;
         r.dst[r.n] = work + at;
-        r.rows[r.n] = rows; r.cols[r.n] = cols; r.lds[r.n] = ld; r.ldd[r.n] = up(cols, 8);
+        r.rows[r.n] = rows; r.cols[r.n] = cols; r.lds[r.n] = ld; r.ldd[r.n] = up(cols, SLICE);
+        r.rows_out[r.n] = up(rows, SLICE);
         ++r.n;
         src = work + at;
     };
     if (p.copy_x) {
         add(o.X, p.M, p.K, o.ldx, p.x_at);
-        o.ldx = up(p.K, 8);
+        o.ldx = up(p.K, SLICE);
     }
     if (p.copy_w) {
         add(o.Wg, p.w_rows, p.w_cols, o.ldw, p.wg_at);
         add(o.Wu, p.w_rows, p.w_cols, o.ldw, p.wu_at);
-        o.ldw = up(p.w_cols, 8);
+        o.ldw = up(p.w_cols, SLICE);
     }
     return r.n > 0 ? status(mgemm::launch_repack(r, s)) : MGEMM_SUCCESS;
 }
@@ -185,6 +214,11 @@ mgemm_status_t check_work(const Plan& p, void* work, int64_t bytes, char** out) 
 
 namespace mgemm {
 
+bool block_has(BlockForm f, int bm, int bn) {
+    if (bm == 256) return bn == 256 || bn == 192;
+    return bm == 128 && (bn == 128 || bn == (f == BLOCK_FORWARD || f == BLOCK_AGAIN ? 256 : 192));
+}
+
 int block_splits(int64_t slices, int requested) {
     if (requested <= 1 || slices < 2) return 1;
     const int64_t ks = requested < slices ? requested : slices, nks = (slices + ks - 1) / ks;
@@ -192,7 +226,7 @@ int block_splits(int64_t slices, int requested) {
 }
 
 int64_t block_tiles(BlockForm f, const BlockArgs& a, BlockTile t) {
-    const int out = f == BLOCK_FORWARD || f == BLOCK_AGAIN ? 96 : t.bn;
+    const int out = f == BLOCK_FORWARD || f == BLOCK_AGAIN ? t.bn / 2 : t.bn;
     return (a.M + t.bm - 1) / t.bm * a.batches_m * ((a.N + out - 1) / out * a.batches_n);
 }
 
@@ -217,6 +251,19 @@ mgemm_status_t mgemm_gated_workspace(mgemm_layout_t layoutW, int64_t M, int64_t 
     return MGEMM_SUCCESS;
 }
 
+mgemm_status_t mgemm_set_gated_tile(mgemm_handle_t h, int32_t product, int32_t rows, int32_t columns,
+                                    int32_t ksplit) {
+    if (!h || product < 0 || product > 2 || ksplit < 0 || ksplit > MGEMM_MAX_KSPLIT) return MGEMM_ERR_INVALID_ARG;
+    if (rows != 0) {
+        const BlockForm f = product == 0 ? mgemm::BLOCK_FORWARD : product == 1 ? mgemm::BLOCK_DX : mgemm::BLOCK_DW;
+        if (!mgemm::block_has(f, rows, columns)) return MGEMM_ERR_UNSUPPORTED;
+    } else if (columns != 0 || ksplit != 0) {
+        return MGEMM_ERR_INVALID_ARG;
+    }
+    h->gated_tile[product] = mgemm_host::GatedTile{rows, columns, ksplit};
+    return MGEMM_SUCCESS;
+}
+
 mgemm_status_t mgemm_gated_forward(mgemm_handle_t h, mgemm_layout_t layoutW, int64_t M, int64_t N, int64_t K,
                                    const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, void* Z,
                                    int64_t ldz, void* G, void* U, int64_t ldg, mgemm_dtype_t dtype, void* work,
@@ -238,17 +285,16 @@ mgemm_status_t mgemm_gated_forward(mgemm_handle_t h, mgemm_layout_t layoutW, int
     const Plan p = make_plan(layoutW, M, N, K, X, ldx, Wg, Wu, ldw, true, false, false, false);
     char* w;
     if (const mgemm_status_t st = check_work(p, work, work_bytes, &w); st != MGEMM_SUCCESS) return st;
+    BlockArgs a = base_args(h->ws, M, N, p.copy_x && p.copy_w ? up(K, SLICE) : K);
+    const BlockTile t = choose(h, mgemm::BLOCK_FORWARD, a);
+    if (t.ks < 1) return MGEMM_ERR_UNSUPPORTED;
     Operands o{X, Wg, Wu, ldx, ldw};
     if (const mgemm_status_t st = lay_out(p, w, o, stream); st != MGEMM_SUCCESS) return st;
-    BlockArgs a = base_args(h->ws);
-    a.M = M; a.N = N; a.K = K;
     a.A[0] = a.A[1] = o.X; a.lda = o.ldx;
     a.B[0] = o.Wg; a.B[1] = o.Wu; a.ldb = o.ldw;
-    a.Mr = up(M, 8); a.Nr = up(N, 8);
     a.Z = Z; a.ldz = ldz;
     a.C[0] = G; a.C[1] = U; a.ldc = ldg;
-    return status(mgemm::launch_block_forward(a, (int)dtype, p.col, false,
-                                              choose(h->num_cu, mgemm::BLOCK_FORWARD, a, h->ws), stream));
+    return status(mgemm::launch_block_forward(a, (int)dtype, p.col, false, t, stream));
 }
 
 mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, int64_t M, int64_t N, int64_t K,
@@ -276,61 +322,56 @@ mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, in
     const Plan p = make_plan(layoutW, M, N, K, X, ldx, Wg, Wu, ldw, false, again, dX != nullptr, dWg != nullptr);
     char* w;
     if (const mgemm_status_t st = check_work(p, work, work_bytes, &w); st != MGEMM_SUCCESS) return st;
+    // Extents of dG and dU that the products see: padded with zeros where the
+    // operand they meet is.
+    const int64_t Mp = p.copy_x ? p.d_rows : M, Np = p.copy_w ? p.d_cols : N, ldd = p.d_cols;
+    BlockArgs fa = base_args(h->ws, Mp, Np, p.copy_x && p.copy_w ? up(K, SLICE) : K), xa = base_args(h->ws, M, K, Np),
+              wa = col ? base_args(h->ws, N, K, Mp) : base_args(h->ws, K, N, Mp);
+    (col ? wa.batches_m : wa.batches_n) = 2;
+    const BlockTile ft = again ? choose(h, mgemm::BLOCK_AGAIN, fa) : BlockTile{0, 0, 1};
+    BlockTile xt{0, 0, 1}, wt{0, 0, 1};
+    bool pair = false;
+    if (dX) xt = choose(h, mgemm::BLOCK_DX, xa);
+    if (dWg) wt = choose(h, mgemm::BLOCK_DW, wa);
+    if (dX && dWg) pair = choose_pair(h, xa, wa, xt, wt);
+    if (ft.ks < 1 || xt.ks < 1 || wt.ks < 1) return MGEMM_ERR_UNSUPPORTED;
     Operands o{X, Wg, Wu, ldx, ldw};
     if (const mgemm_status_t st = lay_out(p, w, o, stream); st != MGEMM_SUCCESS) return st;
     void *dG = w + p.dg_at, *dU = w + p.du_at;
 
+    hipError_t e;
     if (again) {
-        BlockArgs a = base_args(h->ws);
-        a.M = M; a.N = N; a.K = K;
-        a.A[0] = a.A[1] = o.X; a.lda = o.ldx;
-        a.B[0] = o.Wg; a.B[1] = o.Wu; a.ldb = o.ldw;
-        a.Mr = up(M, 8); a.Nr = up(N, 8);
-        a.dZ = dZ; a.ldz = lddz;
-        a.C[0] = dG; a.C[1] = dU; a.ldc = p.ldd;
-        if (hipError_t e = mgemm::launch_block_forward(a, (int)dtype, col, true,
-                                                       choose(h->num_cu, mgemm::BLOCK_AGAIN, a, h->ws), stream);
-            e != hipSuccess)
-            return MGEMM_ERR_HIP;
-    } else if (hipError_t e = mgemm::launch_gated_grad(M, N, G, U, ldg, dZ, lddz, dG, dU, p.ldd, (int)dtype, stream);
-               e != hipSuccess) {
-        return MGEMM_ERR_HIP;
+        fa.A[0] = fa.A[1] = o.X; fa.lda = o.ldx;
+        fa.B[0] = o.Wg; fa.B[1] = o.Wu; fa.ldb = o.ldw;
+        fa.dZ = dZ; fa.ldz = lddz;
+        fa.Mz = M; fa.Nz = N;
+        fa.C[0] = dG; fa.C[1] = dU; fa.ldc = ldd;
+        e = mgemm::launch_block_forward(fa, (int)dtype, col, true, ft, stream);
+    } else {
+        e = mgemm::launch_gated_grad(M, N, p.d_rows, p.d_cols, G, U, ldg, dZ, lddz, dG, dU, ldd, (int)dtype, stream);
     }
-    if (dX) {
-        BlockArgs a = base_args(h->ws);
-        a.M = M; a.N = K; a.K = N;
-        a.A[0] = dG; a.A[1] = dU; a.lda = p.ldd;
-        a.B[0] = o.Wg; a.B[1] = o.Wu; a.ldb = o.ldw;
-        a.Mr = up(M, 8); a.Nr = up(K, 8);
-        a.C[0] = a.C[1] = dX; a.ldc = lddx;
-        // Row-major weights (in x out) are contiguous along this contraction.
-        if (hipError_t e = mgemm::launch_block_dx(a, (int)dtype, !col, choose(h->num_cu, mgemm::BLOCK_DX, a, h->ws),
-                                                  stream);
-            e != hipSuccess)
-            return MGEMM_ERR_HIP;
+    if (e != hipSuccess) return MGEMM_ERR_HIP;
+    const void* d[2] = {dG, dU};
+    for (int i = 0; i < 2; ++i) {
+        xa.A[i] = d[i];
+        xa.B[i] = i ? o.Wu : o.Wg;
+        xa.C[i] = dX;
+        wa.A[i] = col ? d[i] : o.X;
+        wa.B[i] = col ? o.X : d[i];
+        wa.C[i] = i ? dWu : dWg;
     }
-    if (dWg) {
-        BlockArgs a = base_args(h->ws);
-        a.K = M;
-        a.beta = beta;
-        a.C[0] = dWg; a.C[1] = dWu; a.ldc = lddw;
-        if (col) {
-            a.M = N; a.N = K;
-            a.A[0] = dG; a.A[1] = dU; a.lda = p.ldd;
-            a.B[0] = a.B[1] = o.X; a.ldb = o.ldx;
-            a.batches_m = 2;
-        } else {
-            a.M = K; a.N = N;
-            a.A[0] = a.A[1] = o.X; a.lda = o.ldx;
-            a.B[0] = dG; a.B[1] = dU; a.ldb = p.ldd;
-            a.batches_n = 2;
-        }
-        a.Mr = up(a.M, 8); a.Nr = up(a.N, 8);
-        if (hipError_t e = mgemm::launch_block_dw(a, (int)dtype, choose(h->num_cu, mgemm::BLOCK_DW, a, h->ws), stream);
-            e != hipSuccess)
-            return MGEMM_ERR_HIP;
-    }
-    return MGEMM_SUCCESS;
+    xa.lda = ldd;
+    xa.ldb = o.ldw;
+    xa.ldc = lddx;
+    wa.lda = col ? ldd : o.ldx;
+    wa.ldb = col ? o.ldx : ldd;
+    wa.ldc = lddw;
+    wa.beta = beta;
+    // Row-major weights (in x out) are contiguous along dX's contraction.
+    if (pair) return status(mgemm::launch_block_pair(xa, wa, (int)dtype, !col, xt.ks, wt.ks, stream));
+    if (dX) e = mgemm::launch_block_dx(xa, (int)dtype, !col, xt, stream);
+    if (dWg && e == hipSuccess) e = mgemm::launch_block_dw(wa, (int)dtype, wt, stream);
+    return status(e);
 }
 
 }  // extern "C"

@@ -1,7 +1,7 @@
 // Tile loop of the gated block's products (k_gated_forward.hip, k_gated_dx.hip,
-// k_gated_dw.hip): 16-bit operands copied straight into a four-slot LDS ring
-// of 32-element slices, fragments read one K-step ahead of the MFMAs that use
-// them, one workgroup barrier per slice, and the order of copies, reads and
+// k_gated_dw.hip): 16-bit operands copied straight into an LDS ring of
+// slices of 32 or 64 elements, fragments read ahead of the MFMAs that use them,
+// one workgroup barrier per slice, and the order of copies, reads and
 // MFMAs pinned so that one wave per SIMD keeps its matrix core fed: the
 // schedule and LDS layouts of k_h_dma.hip.  What differs is how operands are
 // found:
@@ -28,34 +28,59 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int BK = 32, NT = 256;
-constexpr int SLOTS = 4, AHEAD = SLOTS - 1;      // slices in flight
-constexpr int ROW = BK * 2;                      // bytes of a K-contiguous row of a slice
+constexpr int NT = 256;
 constexpr int SPLIT_GROUP_M = 2, UNSPLIT_GROUP_M = 4;   // tile orders of k_h_dma.hip
+constexpr int LDS_MAX = 160 * 1024;
 
 template <int FORM>
 constexpr bool is_dual() { return FORM == BLOCK_FORWARD || FORM == BLOCK_AGAIN; }
 
-// Plain forms: waves 2x2.  Forward: waves 4x1, a wave holds all 192 columns.
+// Waves are 2x2.  A forward tile's B slot holds BN/2 columns of Wg, then the
+// same BN/2 of Wu; a wave takes the same columns of both, so that G and U of
+// an output are in matching registers of one lane.  With BN = 192 the 96
+// columns of each do not halve into 32-column blocks: waves are then 4x1, a
+// wave holds BM/4 rows of all of them.
 template <int FORM, int BM_, int BN_>
 struct Cfg {
     static constexpr bool DUAL = is_dual<FORM>();
     static constexpr int BM = BM_, BN = BN_;
-    static_assert(BN == 256 || BN == 192, "tile width");
-    static_assert(!DUAL || BN == 192, "the forward pair uses the 192-wide slot");
+    static_assert(BN == 256 || BN == 192 || BN == 128, "tile width");
     static_assert(BM == 256 || BM == 128, "tile height");
-    static constexpr int A_BYTES = BM * ROW, A_COPIES = BM / 64;     // 1 KiB copies per wave per slice
+    static constexpr bool TALL = DUAL && BN == 192;                  // waves 4x1
+    static constexpr int BK = slice_of(BM), KS = BK / 16;            // elements and K-steps of a slice
+    static constexpr int ROW = BK * 2;                               // bytes of a K-contiguous row of a slice
+    static constexpr int A_BYTES = BM * ROW, A_COPIES = A_BYTES / 4096;   // 1 KiB copies per wave per slice
     static constexpr int B_ROW = BN * 2, B_CHUNKS = BN / 8;
-    static constexpr int B_BYTES = BK * B_ROW, B_COPIES = BN / 64;
+    static constexpr int B_BYTES = BK * B_ROW, B_COPIES = B_BYTES / 4096;
     static constexpr int COPIES = A_COPIES + B_COPIES;
-    static constexpr int SLOT_BYTES = A_BYTES + B_BYTES, LDS = SLOTS * SLOT_BYTES;
-    static constexpr int WROWS = DUAL ? BM / 4 : BM / 2;
-    static constexpr int TM = WROWS / 32, TN = DUAL ? BN / 32 : BN / 64;
-    static constexpr int WN = DUAL ? 0 : BN / 2;
-    static constexpr int OUT = DUAL ? BN / 2 : BN;
+    static constexpr int SLOT_BYTES = A_BYTES + B_BYTES;
+    // As many slices in flight as fit: all workgroups of an XCD walk the
+    // contraction together, so each slice's first request goes to memory
+    // (1 to 2 us under load), and a small tile's slice lasts 0.2 us.
+    static constexpr int SLOTS = LDS_MAX / SLOT_BYTES < 8 ? LDS_MAX / SLOT_BYTES : 8, AHEAD = SLOTS - 1;
+    static constexpr int WROWS = TALL ? BM / 4 : BM / 2;
+    static constexpr int TM = WROWS / 32, TN = TALL ? BN / 32 : BN / 64;
+    static constexpr int OUT = DUAL ? BN / 2 : BN;                   // output columns of a tile
+    static constexpr int WOUT = TALL ? OUT : OUT / 2;                // of a wave
+    static constexpr int TNO = DUAL ? TN / 2 : TN;                   // 32-column output blocks of a wave
+    static constexpr int STAGE_ROW = WOUT * 2 + 16;                  // bytes of a staged row of outputs
+    static constexpr int LDS = SLOTS * SLOT_BYTES;
+    static_assert(4 * 3 * 32 * STAGE_ROW <= LDS, "outputs are staged in the ring");
+    // Slot column of a wave's 32-column block t.
+    static __device__ __forceinline__ int column(int wn, int t) {
+        if constexpr (TALL) return 32 * t;
+        else if constexpr (DUAL) return (t < TNO ? 0 : OUT) + WOUT * wn + 32 * (t % TNO);
+        else return WOUT * wn + 32 * t;
+    }
 };
 
-__device__ __forceinline__ int row_swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
+// Chunk c of a K-contiguous row r is at position c ^ row_swz(r): the 16-byte
+// reads of a wave hit every bank once per 16 lanes.
+template <int BK>
+__device__ __forceinline__ int row_swz(int r) {
+    if constexpr (BK == 64) return (r >> 1) & 7;
+    else return ((r >> 1) ^ (r >> 2)) & 3;
+}
 // Chunk position of chunk c in K-row k of a slot whose K-rows are W elements
 // wide (an involution for each k): free of bank conflicts for the transposed reads.
 template <int W>
@@ -79,12 +104,15 @@ __device__ __forceinline__ void wait_vm() {
     static_assert(N >= 0 && N < 64, "vmcnt range");
     __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
-// Waits until at most n slices of L copies each are in flight (copies complete in order).
-template <int L>
+// Waits until at most n <= MAX slices of L copies each are in flight (copies complete in order).
+template <int L, int MAX>
 __device__ __forceinline__ void wait_slices(int n) {
-    if (n <= 0) wait_vm<0>();
-    else if (n == 1) wait_vm<L>();
-    else wait_vm<2 * L>();
+    if constexpr (MAX == 0) {
+        wait_vm<0>();
+    } else {
+        if (n >= MAX) wait_vm<L * MAX>();
+        else wait_slices<L, MAX - 1>(n);
+    }
 }
 __device__ __forceinline__ void fence_sched() {
     __builtin_amdgcn_sched_barrier(0);
@@ -93,6 +121,33 @@ __device__ __forceinline__ void fence_sched() {
 __device__ __forceinline__ void slice_barrier() {
     fence_sched();
     __builtin_amdgcn_s_barrier();
+    fence_sched();
+}
+
+// Orders LDS accesses between the lanes of one wave: the hardware keeps a
+// wave's LDS operations in order, so only the compiler has to be told.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// A value into, and out of, an accumulator register at this point of the
+// program.  Left to itself the compiler moves a whole tile's accumulators to
+// vector registers before the first use, more than there are.
+__device__ __forceinline__ float in_acc(float x) {
+    asm volatile("" : "+a"(x));
+    return x;
+}
+__device__ __forceinline__ float from_acc(float x) {
+    float y;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(y) : "a"(x));
+    return y;
+}
+// Before the first from_acc after MFMAs: longer than a matrix result takes to
+// be readable (the compiler does not see into from_acc).
+__device__ __forceinline__ void acc_settle() {
+    fence_sched();
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     fence_sched();
 }
 
@@ -138,52 +193,51 @@ __device__ __forceinline__ void load4(const uint16_t* row, int n, int lim, bool 
 }
 __device__ __forceinline__ bool vec4_ok(const void* p, int64_t ld) { return ld % 4 == 0 && ((uintptr_t)p & 7) == 0; }
 
-// Stores the outputs of columns n0+ni .. n0+ni+3 of row m from their FP32
-// sums: g alone (dX, dW) or g and u (forward).  Each output is rounded once;
-// Z comes from the unrounded sums, dG and dU from G and U as the forward pass
-// stores them.
+// Four outputs of plane `plane` (forward: Z, G, U; recomputed backward: dG, dU)
+// before their one rounding.  g: the sums of dX, dW or G, or dG; u: of U, or dU.
+// Z comes from the unrounded sums.
 template <int DT, int FORM>
-__device__ __forceinline__ void block_out(const BlockArgs& f, int bt, int64_t m, int64_t n0, int ni, int nlim,
-                                          f32x4 g, f32x4 u) {
-    if (ni >= nlim) return;
+__device__ __forceinline__ void block_value(int plane, f32x4 g, f32x4 u, float (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (FORM == BLOCK_FORWARD) v[e] = plane == 0 ? silu_f32<DT>(g[e]) * u[e] : plane == 1 ? g[e] : u[e];
+        else v[e] = plane == 0 ? g[e] : u[e];
+    }
+}
+template <int FORM>
+constexpr int planes() { return FORM == BLOCK_FORWARD ? 3 : FORM == BLOCK_AGAIN ? 2 : 1; }
+// Plane's matrix (null: not stored) and its row stride.
+template <int FORM>
+__device__ __forceinline__ uint16_t* plane_of(const BlockArgs& f, int plane, int bt, int64_t& ld) {
     if constexpr (FORM == BLOCK_FORWARD) {
-        float z[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = silu_f32<DT>(g[e]) * u[e];
-        store_out4<DT, EPI_NONE>((uint16_t*)f.Z + m * f.ldz + n0, ni, nlim, vec4_ok(f.Z, f.ldz), 0.f, z);
-        if (f.C[0] != nullptr) {
-            float a[4] = {g[0], g[1], g[2], g[3]}, b[4] = {u[0], u[1], u[2], u[3]};
-            store_out4<DT, EPI_NONE>((uint16_t*)f.C[0] + m * f.ldc + n0, ni, nlim, vec4_ok(f.C[0], f.ldc), 0.f, a);
-            store_out4<DT, EPI_NONE>((uint16_t*)f.C[1] + m * f.ldc + n0, ni, nlim, vec4_ok(f.C[1], f.ldc), 0.f, b);
-        }
-    } else if constexpr (FORM == BLOCK_AGAIN) {
-        float dz[4], a[4], b[4];
-        load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n0, ni, nlim, vec4_ok(f.dZ, f.ldz), dz);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) gated_grad(round_trip<DT>(g[e]), round_trip<DT>(u[e]), dz[e], a[e], b[e]);
-        store_out4<DT, EPI_NONE>((uint16_t*)f.C[0] + m * f.ldc + n0, ni, nlim, vec4_ok(f.C[0], f.ldc), 0.f, a);
-        store_out4<DT, EPI_NONE>((uint16_t*)f.C[1] + m * f.ldc + n0, ni, nlim, vec4_ok(f.C[1], f.ldc), 0.f, b);
+        ld = plane == 0 ? f.ldz : f.ldc;
+        return (uint16_t*)(plane == 0 ? f.Z : plane == 1 ? f.C[0] : f.C[1]);
     } else {
-        float v[4] = {g[0], g[1], g[2], g[3]};
-        store_out4<DT, EPI_NONE>((uint16_t*)f.C[bt] + m * f.ldc + n0, ni, nlim, vec4_ok(f.C[bt], f.ldc), f.beta, v);
+        ld = f.ldc;
+        return (uint16_t*)((FORM == BLOCK_AGAIN ? plane : bt) ? f.C[1] : f.C[0]);
     }
 }
 
-template <int DT, int FORM, int BM, int BN, bool AMC, bool BKC, bool PARTIAL>
-__global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
+// What a workgroup stores: outputs, partial sums, or what f.ksplit says.
+enum Store : int { STORE_OUT = 0, STORE_PART = 1, STORE_EITHER = 2 };
+
+// Workgroup bid of nblocks.
+template <int DT, int FORM, int BM, int BN, bool AMC, bool BKC, int STORE>
+__device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblocks, unsigned char* smem) {
     using G = Cfg<FORM, BM, BN>;
     constexpr bool DUAL = G::DUAL;
     constexpr int SEGS = FORM == BLOCK_DX ? 2 : 1;
     static_assert(!(AMC && (BKC || DUAL)), "operand forms");
     constexpr int TM = G::TM, TN = G::TN, COPIES = G::COPIES, A_COPIES = G::A_COPIES;
+    constexpr int SLOTS = G::SLOTS, AHEAD = G::AHEAD, BK = G::BK, KS = G::KS, ROW = G::ROW;
+    constexpr int RCH = ROW / 16, RPC = 64 / RCH;        // chunks of a K-contiguous row, and rows per copy
     constexpr int A_BYTES = G::A_BYTES, A_KROW = BM * 2, A_CHUNKS = BM / 8, B_ROW = G::B_ROW;
     using Fr = Frags<TM, TN>;
-    extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = DUAL ? wave : wave >> 1, wn = DUAL ? 0 : wave & 1;
+    const int wm = G::TALL ? wave : wave >> 1, wn = G::TALL ? 0 : wave & 1;
     const int tiles_m = (int)((f.M + BM - 1) / BM), tiles_n = (int)((f.N + G::OUT - 1) / G::OUT);
-    const int pos = xcd_linear(blockIdx.x, gridDim.x);
+    const int pos = xcd_linear(bid, nblocks);
     const int split = pos % f.ksplit;
     int tmi, tni;
     tile_from_linear(pos / f.ksplit, tiles_m * f.batches_m, tiles_n * f.batches_n,
@@ -205,7 +259,7 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
     const int64_t b_diff = (const char*)f.B[1] - (const char*)f.B[0];
 
     // Copies of this wave, 1 KiB each (16 bytes a lane).  K-contiguous
-    // operands: 16 rows of 64 bytes, lane l takes row l/4's chunk (l%4 ^ swz);
+    // operands: whole rows of a slice, their chunks swizzled;
     // the others: 64 consecutive chunk positions of the slot.  Rows and
     // chunks past the edge read the last valid ones.
     const char* src[COPIES];
@@ -220,8 +274,8 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
             src[i] = A + ((int64_t)k * f.lda + m0 + 8 * c) * 2;
             dst[i] = j * 1024;
         } else {
-            const int r0 = BM / 4 * wave + 16 * i, r = r0 + (lane >> 2);
-            const int c = (lane & 3) ^ row_swz(r);
+            const int r0 = BM / 4 * wave + RPC * i, r = r0 + lane / RCH;
+            const int c = lane % RCH ^ row_swz<BK>(r);
             src[i] = A + ((m0 + (r < mlim ? r : mlim - 1)) * f.lda + 8 * c) * 2;
             dst[i] = r0 * ROW;
         }
@@ -229,8 +283,8 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
 #pragma unroll
     for (int i = 0; i < G::B_COPIES; ++i) {
         if constexpr (BKC) {
-            const int r0 = BN / 4 * wave + 16 * i, r = r0 + (lane >> 2);
-            const int c = (lane & 3) ^ row_swz(r);
+            const int r0 = BN / 4 * wave + RPC * i, r = r0 + lane / RCH;
+            const int c = lane % RCH ^ row_swz<BK>(r);
             const bool second = DUAL && r >= G::OUT;
             int rr = second ? r - G::OUT : r;
             rr = rr < nlim ? rr : nlim - 1;
@@ -252,18 +306,18 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
     // Byte offsets of slice j (of the whole contraction) from src.
     auto a_at = [&](int j) { return SEGS == 2 && j >= nk_seg ? a_diff + (j - nk_seg) * a_step : j * a_step; };
     auto b_at = [&](int j) { return SEGS == 2 && j >= nk_seg ? b_diff + (j - nk_seg) * b_step : j * b_step; };
-    auto copy = [&](int s, int i) {
+    auto copy = [&](int s, int slot, int i) {
         copy_to_lds(src[i] + (i < A_COPIES ? a_at(j0 + s) : b_at(j0 + s)),
-                    lds0 + (unsigned)(s % SLOTS) * G::SLOT_BYTES + dst[i]);
+                    lds0 + (unsigned)slot * G::SLOT_BYTES + dst[i]);
     };
 
     // Fragment read offsets within a slot.
-    int a_off[TM][2][AMC ? 2 : 1], b_off[TN][2][BKC ? 1 : 2];
+    int a_off[TM][KS][AMC ? 2 : 1], b_off[TN][KS][BKC ? 1 : 2];
     const int q4 = lane >> 4, t16 = lane & 15;
 #pragma unroll
     for (int t = 0; t < TM; ++t)
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+        for (int ks = 0; ks < KS; ++ks) {
             if constexpr (AMC) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -273,21 +327,21 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
                 }
             } else {
                 const int r = G::WROWS * wm + 32 * t + (lane & 31);
-                a_off[t][ks][0] = r * ROW + (((2 * ks + (lane >> 5)) ^ row_swz(r)) << 4);
+                a_off[t][ks][0] = r * ROW + (((2 * ks + (lane >> 5)) ^ row_swz<BK>(r)) << 4);
             }
         }
 #pragma unroll
     for (int t = 0; t < TN; ++t)
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+        for (int ks = 0; ks < KS; ++ks) {
             if constexpr (BKC) {
-                const int r = G::WN * wn + 32 * t + (lane & 31);
-                b_off[t][ks][0] = A_BYTES + r * ROW + (((2 * ks + (lane >> 5)) ^ row_swz(r)) << 4);
+                const int r = G::column(wn, t) + (lane & 31);
+                b_off[t][ks][0] = A_BYTES + r * ROW + (((2 * ks + (lane >> 5)) ^ row_swz<BK>(r)) << 4);
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int k = ks * 16 + 8 * (q4 >> 1) + 4 * h + (t16 >> 2);
-                    const int n = G::WN * wn + 32 * t + 16 * (q4 & 1) + 4 * (t16 & 3);
+                    const int n = G::column(wn, t) + 16 * (q4 & 1) + 4 * (t16 & 3);
                     b_off[t][ks][h] = A_BYTES + k * B_ROW + (chunk_pos<BN>(n >> 3, k) << 4) + ((n & 7) << 1);
                 }
             }
@@ -299,10 +353,10 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
                                                     (__attribute__((address_space(3))) i16x4*)hi));
         return i32x4{l.x, l.y, h.x, h.y};
     };
-    // Read r of (slice s, K-step ks), in the order the next K-step needs them:
+    // Read r of K-step ks of a slot, in the order the next K-step needs them:
     // A0, B0 .. B(TN-1), A1 .. A(TM-1).
-    auto read = [&](Fr& fr, int s, int ks, int r) {
-        const unsigned char* base = smem + (s % SLOTS) * G::SLOT_BYTES;
+    auto read = [&](Fr& fr, int slot, int ks, int r) {
+        const unsigned char* base = smem + slot * G::SLOT_BYTES;
         if (r == 0 || r > TN) {
             const int t = r == 0 ? 0 : r - TN;
             if constexpr (AMC) fr.a[t] = read_tr(base + a_off[t][ks][0], base + a_off[t][ks][AMC]);
@@ -318,11 +372,34 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
+    // beta * C goes into the sum first, so that the stores need no second read.
+    if constexpr (STORE != STORE_PART && FORM == BLOCK_DW) {
+        if (f.beta != 0.0f && f.ksplit == 1) {
+            int64_t ld;
+            const uint16_t* C = plane_of<FORM>(f, 0, bt, ld);
+            const bool ok = vec4_ok(C, ld);
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm) {
+                const int mi = G::WROWS * wm + 32 * tm + (lane & 31);
+                if (mi >= mlim) continue;
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float c[4];
+                        load4<DT>(C + (m0 + mi) * ld + n0, G::column(wn, tn) + 8 * q + 4 * (lane >> 5), nlim, ok, c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[tm][tn][4 * q + e] = in_acc(f.beta * c[e]);
+                    }
+            }
+        }
+    }
 
-    // One K-step: the MFMAs on `use`, with the reads of (rs, rks) and the
-    // copies c0 .. c1-1 of slice cs spread between them.
+    // One K-step: the MFMAs on `use`, with the reads of (slot rs, K-step rks)
+    // and the copies c0 .. c1-1 of slice cs (into slot cslot) spread between them.
     constexpr int NM = TM * TN, NR = TM + TN;
-    auto kstep = [&](const Fr& use, Fr& nxt, bool do_read, int rs, int rks, bool do_copy, int cs, int c0, int c1) {
+    auto kstep = [&](const Fr& use, Fr& nxt, bool do_read, int rs, int rks, bool do_copy, int cs, int cslot, int c0,
+                     int c1) {
 #pragma unroll
         for (int i = 0; i < NM; ++i) {
             const int tm = i / TN, tn = (tm & 1) ? TN - 1 - i % TN : i % TN;
@@ -330,7 +407,7 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
             if (do_copy) {
 #pragma unroll
                 for (int c = c0; c < c1; ++c)
-                    if (i == (c - c0) * NM / (c1 - c0)) copy(cs, c);
+                    if (i == (c - c0) * NM / (c1 - c0)) copy(cs, cslot, c);
             }
             if (do_read) {
 #pragma unroll
@@ -341,40 +418,49 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
         }
     };
 
-    // Prologue: request slices 0 .. AHEAD-1, make slice 0 visible, read its first fragments.
-    Fr f0, f1;
+    // Prologue: request slices 0 .. AHEAD-1, make slice 0 visible, read its fragments.
+    Fr fr[2];
     const int npro = nk < AHEAD ? nk : AHEAD;
     for (int s = 0; s < npro; ++s)
-        for (int i = 0; i < COPIES; ++i) copy(s, i);
+        for (int i = 0; i < COPIES; ++i) copy(s, s, i);
     if (nk > 0) {
-        wait_slices<COPIES>(npro - 1);
+        wait_slices<COPIES, AHEAD - 1>(npro - 1);
         slice_barrier();
 #pragma unroll
-        for (int r = 0; r < NR; ++r) read(f0, 0, 0, r);
+        for (int r = 0; r < NR; ++r) read(fr[0], 0, 0, r);
     }
-    // Slice j: wait for this wave's copies of slice j+1 (later ones may stay
-    // in flight), barrier (slice j+1 visible, the slot of slice j-1 free),
-    // then K-step 0 with the A copies of slice j+AHEAD and K-step 1 with its
-    // B copies.
-    int j = 0;
+    // Slice j (slot cur): wait for this wave's copies of slice j+1 (later ones
+    // may stay in flight), barrier (slice j+1 visible, the slot `old` of slice
+    // j-1 free), then the K-steps, which read the next K-step's fragments and
+    // issue the copies of slice j+AHEAD a few at a time.
+    int j = 0, cur = 0, old = SLOTS - 1;
     for (; j + AHEAD < nk; ++j) {
-        wait_slices<COPIES>(AHEAD - 2);
+        const int nxt = cur + 1 == SLOTS ? 0 : cur + 1;
+        wait_vm<COPIES * (AHEAD - 2)>();
         slice_barrier();
-        kstep(f0, f1, true, j, 1, true, j + AHEAD, 0, A_COPIES);
-        kstep(f1, f0, true, j + 1, 0, true, j + AHEAD, A_COPIES, COPIES);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            kstep(fr[ks & 1], fr[~ks & 1], true, ks + 1 < KS ? cur : nxt, (ks + 1) % KS, true, j + AHEAD, old,
+                  ks * COPIES / KS, (ks + 1) * COPIES / KS);
+        old = cur;
+        cur = nxt;
     }
     for (; j < nk; ++j) {
+        const int nxt = cur + 1 == SLOTS ? 0 : cur + 1;
         const bool next = j + 1 < nk;
         if (next) {
-            wait_slices<COPIES>(nk - j - 2);
+            wait_slices<COPIES, AHEAD - 2>(nk - j - 2);
             slice_barrier();
         }
-        kstep(f0, f1, true, j, 1, false, 0, 0, 1);
-        kstep(f1, f0, next, j + 1, 0, false, 0, 0, 1);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            kstep(fr[ks & 1], fr[~ks & 1], ks + 1 < KS || next, ks + 1 < KS ? cur : nxt, (ks + 1) % KS, false, 0, 0, 0,
+                  1);
+        cur = nxt;
     }
 
     // Contraction tail: the range that ends at the last whole slice adds the
-    // remaining K % 32 of every segment, staged by ordinary loads into the
+    // remaining K % BK of every segment, staged by ordinary loads into the
     // positions that the copies fill, zeros past K in both operands (only
     // k < K is read).  No copy is in flight any more.
     const int ktail = (int)(f.K - (int64_t)nk_seg * BK);
@@ -395,8 +481,8 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
                                        : (64 * (wave * G::B_COPIES + ib) + lane) / G::B_CHUNKS;
                     if (k < ktail) v = *(const i32x4*)s;
                 } else {
-                    const int r = is_a ? BM / 4 * wave + 16 * i + (lane >> 2) : BN / 4 * wave + 16 * ib + (lane >> 2);
-                    const int k = 8 * ((lane & 3) ^ row_swz(r));
+                    const int r = (is_a ? BM / 4 * wave + RPC * i : BN / 4 * wave + RPC * ib) + lane / RCH;
+                    const int k = 8 * (lane % RCH ^ row_swz<BK>(r));
                     if (k + 8 <= ktail) {
                         v = *(const i32x4*)s;
                     } else if (k < ktail) {
@@ -410,14 +496,15 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
             }
             __syncthreads();
 #pragma unroll
-            for (int r = 0; r < NR; ++r) read(f0, 0, 0, r);
-            kstep(f0, f1, true, 0, 1, false, 0, 0, 1);
-            kstep(f1, f0, false, 0, 0, false, 0, 0, 1);
+            for (int r = 0; r < NR; ++r) read(fr[0], 0, 0, r);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                kstep(fr[ks & 1], fr[~ks & 1], ks + 1 < KS, 0, (ks + 1) % KS, false, 0, 0, 0, 1);
         }
     }
 
     // Lane holds C(m, n..n+3), m = row within the 32x32 block.
-    if constexpr (PARTIAL) {
+    if (STORE == STORE_PART || (STORE == STORE_EITHER && f.ksplit > 1)) {
         float* d = f.part + ((int64_t)tile * f.ksplit + split) * (int64_t)(NT * TM * TN * 16) + 4 * tid;
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm) {
@@ -431,37 +518,121 @@ __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
                         f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
                 }
         }
-    } else {
+        return;
+    }
+    if constexpr (STORE != STORE_PART) {
+        // Outputs go through LDS, 32 rows at a time in each wave's own piece: the
+        // lane layout would store 16 bytes of each of 32 rows at once.  A wave's
+        // LDS operations stay in order, so one piece serves all rows.
+        __syncthreads();
+        acc_settle();
+        constexpr int NP = planes<FORM>(), PIECE = 32 * G::STAGE_ROW;
+        unsigned char* st = smem + wave * NP * PIECE;
+        const int wrow0 = G::WROWS * wm, wcol0 = G::WOUT * wn;       // this wave's corner of the tile
+        const int cols = nlim - wcol0 < G::WOUT ? nlim - wcol0 : G::WOUT;
+        uint16_t* corner[NP];
+        int64_t ld[NP];
+        bool vec[NP], keep[NP];
+#pragma unroll
+        for (int pl = 0; pl < NP; ++pl) {
+            uint16_t* C = plane_of<FORM>(f, pl, bt, ld[pl]);
+            keep[pl] = C != nullptr;
+            vec[pl] = ld[pl] % 8 == 0 && ((uintptr_t)C & 15) == 0;
+            corner[pl] = C + (m0 + wrow0) * ld[pl] + n0 + wcol0;
+        }
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm) {
-            const int mi = G::WROWS * wm + 32 * tm + (lane & 31);
-            if (mi >= mlim) continue;
+            const int r0 = 32 * tm, fr = lane & 31, nq = 4 * (lane >> 5);
+            const int rows = mlim - wrow0 - r0 < 32 ? mlim - wrow0 - r0 : 32;
+            wave_fence();
 #pragma unroll
-            for (int tn = 0; tn < (DUAL ? TN / 2 : TN); ++tn)
+            for (int tn = 0; tn < G::TNO; ++tn)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const f32x16& a = acc[tm][tn];
-                    const f32x16& b = acc[tm][DUAL ? tn + TN / 2 : tn];
-                    block_out<DT, FORM>(f, bt, m0 + mi, n0, G::WN * wn + 32 * tn + 8 * q + 4 * (lane >> 5), nlim,
-                                        f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]},
-                                        f32x4{b[4 * q], b[4 * q + 1], b[4 * q + 2], b[4 * q + 3]});
+                    f32x4 g, u = f32x4{};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        g[e] = from_acc(acc[tm][tn][4 * q + e]);
+                        if constexpr (DUAL) u[e] = from_acc(acc[tm][tn + TN - G::TNO][4 * q + e]);
+                    }
+                    const int c = 32 * tn + 8 * q + nq;
+                    if constexpr (FORM == BLOCK_AGAIN) {
+                        float dz[4] = {};
+                        const int64_t m = m0 + wrow0 + r0 + fr;
+                        if (m < f.Mz)
+                            load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n0, wcol0 + c,
+                                      (int)(f.Nz - n0 < G::OUT ? f.Nz - n0 : G::OUT), vec4_ok(f.dZ, f.ldz), dz);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float a, b;
+                            gated_grad(round_trip<DT>(g[e]), round_trip<DT>(u[e]), dz[e], a, b);
+                            g[e] = a;
+                            u[e] = b;
+                        }
+                    }
+#pragma unroll
+                    for (int pl = 0; pl < NP; ++pl) {
+                        float v[4];
+                        block_value<DT, FORM>(pl, g, u, v);
+                        *(uint2*)(st + pl * PIECE + fr * G::STAGE_ROW + c * 2) =
+                            make_uint2((uint32_t)to_bits<DT>(v[0]) | ((uint32_t)to_bits<DT>(v[1]) << 16),
+                                       (uint32_t)to_bits<DT>(v[2]) | ((uint32_t)to_bits<DT>(v[3]) << 16));
+                    }
                 }
+            wave_fence();
+#pragma unroll
+            for (int pl = 0; pl < NP; ++pl) {
+                if (!keep[pl]) continue;
+                const unsigned char* from = st + pl * PIECE;
+                uint16_t* to = corner[pl] + r0 * ld[pl];
+                if (vec[pl]) {
+                    constexpr int CH = G::WOUT / 8, PER = 32 * CH / 64;      // 16-byte chunks of a row, per lane
+                    u32x4 w[PER];
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        w[i] = *(const u32x4*)(from + (64 * i + lane) / CH * G::STAGE_ROW + (64 * i + lane) % CH * 16);
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int r = (64 * i + lane) / CH, c = (64 * i + lane) % CH * 8;
+                        if (r >= rows || c >= cols) continue;
+                        uint16_t* o = to + r * ld[pl] + c;
+                        if (c + 8 <= cols) {
+                            *(u32x4*)o = w[i];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (c + e < cols) o[e] = (uint16_t)(w[i][e / 2] >> (16 * (e & 1)));
+                        }
+                    }
+                } else {
+                    // Rows that are not 16-byte aligned: consecutive elements by consecutive lanes.
+                    for (int r = 0; r < rows; ++r)
+                        for (int c = lane; c < cols; c += 64)
+                            to[r * ld[pl] + c] = *(const uint16_t*)(from + r * G::STAGE_ROW + c * 2);
+                }
+            }
+            fence_sched();
         }
     }
+}
+
+template <int DT, int FORM, int BM, int BN, bool AMC, bool BKC, int STORE>
+__global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    block_body<DT, FORM, BM, BN, AMC, BKC, STORE>(f, blockIdx.x, gridDim.x, smem);
 }
 
 // Second phase of a split: one thread per 16-byte chunk of a tile's
 // accumulators sums the ranges in range order and stores four outputs.
 template <int DT, int FORM, int BM, int BN>
-__global__ __launch_bounds__(NT) void k_block_reduce(BlockArgs f) {
+__device__ __forceinline__ void reduce_body(const BlockArgs& f, int bid, int nblocks) {
     using G = Cfg<FORM, BM, BN>;
-    constexpr bool DUAL = G::DUAL;
-    constexpr int TM = G::TM, TN = G::TN, TNO = DUAL ? TN / 2 : TN, CH = TM * TNO * 4;
+    constexpr int TM = G::TM, TN = G::TN, TNO = G::TNO, CH = TM * TNO * 4;
     constexpr int64_t TILE = (int64_t)NT * TM * TN * 16;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = DUAL ? wave : wave >> 1, wn = DUAL ? 0 : wave & 1;
+    const int wm = G::TALL ? wave : wave >> 1, wn = G::TALL ? 0 : wave & 1;
     const int tiles_m = (int)((f.M + BM - 1) / BM), tiles_n = (int)((f.N + G::OUT - 1) / G::OUT);
-    const int pos = xcd_linear(blockIdx.x, gridDim.x);
+    const int pos = xcd_linear(bid, nblocks);
     const int c = pos % CH;
     int tmi, tni;
     tile_from_linear(pos / CH, tiles_m * f.batches_m, tiles_n * f.batches_n, SPLIT_GROUP_M, tmi, tni);
@@ -473,7 +644,7 @@ __global__ __launch_bounds__(NT) void k_block_reduce(BlockArgs f) {
     const int64_t m0 = (int64_t)tmi * BM, n0 = (int64_t)tni * G::OUT;
     const int nlim = (int)(f.N - n0 < G::OUT ? f.N - n0 : G::OUT);
     const int64_t m = m0 + G::WROWS * wm + 32 * tm + (lane & 31);
-    const int ni = G::WN * wn + 32 * tn + 8 * q + 4 * (lane >> 5);
+    const int ni = G::WOUT * wn + 32 * tn + 8 * q + 4 * (lane >> 5);
     if (m >= f.M || ni >= nlim) return;
     const float* part = f.part + (int64_t)tile * f.ksplit * TILE + 4 * tid;
     auto sum = [&](int chunk) {
@@ -488,31 +659,70 @@ __global__ __launch_bounds__(NT) void k_block_reduce(BlockArgs f) {
         for (; s < f.ksplit; ++s) a = a + *(const f32x4*)(p + s * TILE);
         return a;
     };
-    const f32x4 g = sum((tm * TN + tn) * 4 + q);
-    if constexpr (DUAL) block_out<DT, FORM>(f, bt, m, n0, ni, nlim, g, sum((tm * TN + tn + TN / 2) * 4 + q));
-    else block_out<DT, FORM>(f, bt, m, n0, ni, nlim, g, g);
+    f32x4 g = sum((tm * TN + tn) * 4 + q);
+    f32x4 u = G::DUAL ? sum((tm * TN + tn + TNO) * 4 + q) : g;
+    if constexpr (FORM == BLOCK_AGAIN) {
+        float dz[4] = {};
+        if (m < f.Mz)
+            load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n0, ni, (int)(f.Nz - n0 < G::OUT ? f.Nz - n0 : G::OUT),
+                      vec4_ok(f.dZ, f.ldz), dz);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float a, b;
+            gated_grad(round_trip<DT>(g[e]), round_trip<DT>(u[e]), dz[e], a, b);
+            g[e] = a;
+            u[e] = b;
+        }
+    }
+#pragma unroll
+    for (int plane = 0; plane < planes<FORM>(); ++plane) {
+        int64_t ld;
+        uint16_t* C = plane_of<FORM>(f, plane, bt, ld);
+        if (FORM == BLOCK_FORWARD && C == nullptr) continue;
+        float v[4];
+        block_value<DT, FORM>(plane, g, u, v);
+        store_out4<DT, EPI_NONE>(C + m * ld + n0, ni, nlim, vec4_ok(C, ld), f.beta, v);
+    }
+}
+
+template <int DT, int FORM, int BM, int BN>
+__global__ __launch_bounds__(NT) void k_block_reduce(BlockArgs f) {
+    reduce_body<DT, FORM, BM, BN>(f, blockIdx.x, gridDim.x);
+}
+
+// Fills in the ranges and returns the workgroups of a launch with ks of them.
+template <int FORM, int BM, int BN>
+int64_t set_ranges(BlockArgs& a, int ks) {
+    using G = Cfg<FORM, BM, BN>;
+    const int64_t slices = (a.K / G::BK) * (FORM == BLOCK_DX ? 2 : 1);
+    a.nks = (int)(ks > 1 ? (slices + ks - 1) / ks : (slices > 0 ? slices : 1));
+    a.ksplit = ks > 1 ? (int)((slices + a.nks - 1) / a.nks) : 1;
+    return ((a.M + BM - 1) / BM) * a.batches_m * (((a.N + G::OUT - 1) / G::OUT) * a.batches_n) * a.ksplit;
+}
+// Workgroups of the second phase, per tile.
+template <int FORM, int BM, int BN>
+constexpr int reduce_chunks() {
+    using G = Cfg<FORM, BM, BN>;
+    return G::TM * G::TNO * 4;
 }
 
 template <int DT, int FORM, int BM, int BN, bool AMC, bool BKC>
 hipError_t launch_block(BlockArgs a, int ks, hipStream_t s) {
     using G = Cfg<FORM, BM, BN>;
-    const int64_t slices = (a.K / BK) * (FORM == BLOCK_DX ? 2 : 1);
-    a.nks = (int)(ks > 1 ? (slices + ks - 1) / ks : (slices > 0 ? slices : 1));
-    a.ksplit = ks > 1 ? (int)((slices + a.nks - 1) / a.nks) : 1;
-    const int64_t tiles = ((a.M + BM - 1) / BM) * a.batches_m * (((a.N + G::OUT - 1) / G::OUT) * a.batches_n);
+    const int64_t wgs = set_ranges<FORM, BM, BN>(a, ks);
     auto go = [&](auto kern, bool (&done)[MAX_DEVICES]) -> hipError_t {
         if (hipError_t e = set_lds_limit_once((const void*)kern, G::LDS, done); e != hipSuccess) return e;
-        hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * a.ksplit)), dim3(NT), G::LDS, s, a);
+        hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(NT), G::LDS, s, a);
         return hipGetLastError();
     };
     if (a.ksplit == 1) {
         static bool done[MAX_DEVICES] = {};
-        return go(k_block<DT, FORM, BM, BN, AMC, BKC, false>, done);
+        return go(k_block<DT, FORM, BM, BN, AMC, BKC, STORE_OUT>, done);
     }
     static bool done[MAX_DEVICES] = {};
-    if (hipError_t e = go(k_block<DT, FORM, BM, BN, AMC, BKC, true>, done); e != hipSuccess) return e;
-    constexpr int CH = G::TM * (G::DUAL ? G::TN / 2 : G::TN) * 4;
-    hipLaunchKernelGGL((k_block_reduce<DT, FORM, BM, BN>), dim3((unsigned)(tiles * CH)), dim3(NT), 0, s, a);
+    if (hipError_t e = go(k_block<DT, FORM, BM, BN, AMC, BKC, STORE_PART>, done); e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_block_reduce<DT, FORM, BM, BN>),
+                       dim3((unsigned)(wgs / a.ksplit * reduce_chunks<FORM, BM, BN>())), dim3(NT), 0, s, a);
     return hipGetLastError();
 }
 

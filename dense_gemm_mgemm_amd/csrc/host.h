@@ -36,6 +36,11 @@ struct Table {
     std::map<TableKey, TableEntry> entries;
 };
 
+// A tile forced on a product of the gated block (mgemm_set_gated_tile); rows 0: none.
+struct GatedTile {
+    int rows, columns, ksplit;
+};
+
 TableKey exact_key(const Problem& p);
 TableKey bucket_key(const Problem& p);
 int ceil_log2(int64_t x);
@@ -49,6 +54,7 @@ struct mgemm_handle_s {
     mgemm_host::Table table;      // measured choices (mgemm_tune / mgemm_table_import)
     unsigned long long* stamps;   // clock-stamp buffer (mgemm_set_clock_stamps), or null
     int64_t stamps_cap;           // workgroups it has room for
+    mgemm_host::GatedTile gated_tile[3] = {};   // of the forward pair, dX and the weights' gradients
 };
 
 namespace mgemm_host {

@@ -614,6 +614,24 @@ mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, in
                                     hipStream_t stream);
 
 /*
+ * mgemm_set_gated_tile -- check and measurement hook: forces the tile of one of
+ * the gated block's products in later calls through this handle, as
+ * mgemm_run_variant does for a plain product (tests run every one).
+ *   product : 0 the forward pair (also where it is computed again), 1 dX,
+ *             2 the weights' gradients;
+ *   rows, columns : 256 x 256 or 256 x 192; 128 x 128; 128 x 256 (product 0) or
+ *             128 x 192 (products 1 and 2); product 0 counts the columns of
+ *             both weights.  0, 0 (ksplit 0) returns to the library's choice.
+ *   ksplit : ranges of the contraction as for mgemm_run_variant; 0 the
+ *            library's choice.  A call whose forced ranges do not fit the
+ *            handle's workspace returns MGEMM_ERR_UNSUPPORTED.
+ * Errors: MGEMM_ERR_INVALID_ARG for a NULL handle or values out of range,
+ * MGEMM_ERR_UNSUPPORTED for a tile that the product does not have.
+ */
+mgemm_status_t mgemm_set_gated_tile(mgemm_handle_t h, int32_t product, int32_t rows,
+                                    int32_t columns, int32_t ksplit);
+
+/*
  * mgemm_run_noalloc -- mgemm_run_variant without a handle and without any
  * device allocation, for callers that cannot allocate: code being captured
  * into a HIP graph, tight serving loops, harnesses that forbid hipMalloc.

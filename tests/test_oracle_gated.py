@@ -54,15 +54,17 @@ def test_workspace_sizes():
     assert workspace() == (0, 0)
     assert workspace(backward=1, stored=1) == (0, 3 * 256)
     assert workspace(backward=1, stored=0) == (0, 3 * 256)
-    # An odd stride or base: X is copied; odd weights: both weights are.
-    assert workspace(ldx=17) == (0, 2 * 256)
-    assert workspace(x=_p(2)) == (0, 2 * 256)
-    assert workspace(wu=_p(4)) == (0, 3 * 256)
+    # A copy is 64 x 64 values.  An odd stride or base: X is copied; odd weights: both weights are.
+    copy = 64 * 64 * 2
+    assert workspace(ldx=17) == (0, copy + 256)
+    assert workspace(x=_p(2)) == (0, copy + 256)
+    assert workspace(wu=_p(4)) == (0, 2 * copy + 256)
     # A length that is not a multiple of 8 along an output axis.
-    assert workspace(N=7) == (0, 3 * 256)
+    assert workspace(N=7) == (0, 2 * copy + 256)
     assert workspace(layout=1, N=7, ldw=16) == (0, 0)
     assert workspace(K=15)[1] == 0                                    # the contraction's tail: in place
-    assert workspace(K=15, backward=1, stored=1) == (0, 4 * 256)      # dW's rows: X is copied
+    # dW's rows: X is copied, and dG and dU (64 x 8) are padded as its rows are.
+    assert workspace(K=15, backward=1, stored=1) == (0, copy + 2 * 1024 + 256)
     assert workspace(M=0, backward=1) == (0, 0)
     assert mg.load().mgemm_gated_workspace(0, 4, 8, 16, _p(), 16, _p(), _p(), 8, 2, 0, 0, None) == INVALID
 
