@@ -125,7 +125,7 @@ def load(path: str | None = None):
     lib.mgemm_gated_workspace.argtypes = gated[1:] + [ci, ctypes.c_int32, ctypes.c_int32, pi64]
     lib.mgemm_gated_forward.argtypes = gated + [vp, i64, vp, vp, i64, ci, vp, i64, vp]
     lib.mgemm_gated_backward.argtypes = gated + [vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, f32, ci, vp, i64, vp]
-    lib.mgemm_set_gated_tile.argtypes = [vp] + [ctypes.c_int32] * 4
+    lib.mgemm_set_gated_tile.argtypes = [vp] + [ctypes.c_int32] * 3
     for name in ("mgemm_gated_workspace", "mgemm_gated_forward", "mgemm_gated_backward", "mgemm_set_gated_tile"):
         getattr(lib, name).restype = ci
     lib.mgemm_status_string.argtypes = [ci]
@@ -163,6 +163,10 @@ def _enum(x, table):
 def _stream(s) -> int | None:
     if s is None:
         import torch
+        # torch.cuda.current_stream().cuda_stream without the Stream object (2.8 us, of a call's 7).
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -441,10 +445,10 @@ def mgemm_gated_backward(h, layout, M, N, K, X, ldx, Wg, Wu, ldw, G, U, ldg, dZ,
         raise MgemmError(st, "mgemm_gated_backward")
 
 
-def mgemm_set_gated_tile(h, product, rows=0, columns=0, ksplit=0) -> None:
+def mgemm_set_gated_tile(h, product, size=0, ksplit=0) -> None:
     """Check hook: forces the tile of a product of the gated block (0 the forward
-    pair, 1 dX, 2 the weights' gradients); rows 0: the library's choice."""
-    st = load().mgemm_set_gated_tile(h, int(product), int(rows), int(columns), int(ksplit))
+    pair, 1 dX, 2 the weights' gradients); 0: the library's choice."""
+    st = load().mgemm_set_gated_tile(h, int(product), int(size), int(ksplit))
     if st != MGEMM_SUCCESS:
         raise MgemmError(st, "mgemm_set_gated_tile")
 

@@ -34,20 +34,14 @@ struct BlockArgs {
 enum BlockForm : int { BLOCK_FORWARD = 0, BLOCK_AGAIN = 1, BLOCK_DX = 2, BLOCK_DW = 3 };
 
 struct BlockTile {
-    int bm, bn;               // rows and B columns of a tile (forward: bn / 2 outputs of each product)
+    int size;                 // rows and B columns of a tile (forward: half of the columns for each product)
     int ks;                   // ranges of the contraction
 };
 
-// Elements of the contraction that a tile of bm rows takes per slice.
-constexpr int slice_of(int bm) { return bm == 256 ? 32 : 64; }
-// Whether a product has a tile of this size.
-bool block_has(BlockForm f, int bm, int bn);
+// Elements of the contraction that a tile takes per slice.
+constexpr int slice_of(int size) { return size == 256 ? 32 : 64; }
 // Ranges that a request for at most `requested` turns into (whole slices per range).
 int block_splits(int64_t slices, int requested);
-// Bytes of the partial sums of a split launch.
-int64_t block_part_bytes(BlockForm f, const BlockArgs& a, BlockTile t);
-// Workgroups of an unsplit launch.
-int64_t block_tiles(BlockForm f, const BlockArgs& a, BlockTile t);
 
 // b_kc: the pair's B matrices (weights) are contiguous along the contraction.
 hipError_t launch_block_forward(const BlockArgs& a, int dtype, bool b_kc, bool again, BlockTile t, hipStream_t s);

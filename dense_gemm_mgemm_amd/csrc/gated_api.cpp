@@ -77,51 +77,107 @@ Plan make_plan(mgemm_layout_t layout, int64_t M, int64_t N, int64_t K, const voi
     return p;
 }
 
-// Tile and split with the smallest predicted time.  The model is that of the
-// 16-bit products: the block's tiles move the same bytes and issue the same
-// matrix instructions per slice.
-BlockTile choose(mgemm_handle_t h, BlockForm form, const BlockArgs& a) {
+// One product's workgroups in tiles of one size and split.
+struct Grid {
+    BlockTile tile;
+    int64_t tiles;
+    int64_t wgs;            // tiles x ranges
+    int64_t part_bytes;     // of the partial sums (0: whole contractions)
+    double wg_us;           // one workgroup
+    double sum_us;          // the second phase
+    double us;              // the launches
+};
+
+// Predicted times (microseconds).  A workgroup takes 0.45 us per 64 elements of
+// the contraction in a 128 tile and 1.45 in a 256 tile, and 3.6 or 7 us from
+// its launch to its first MFMA and through its outputs; a CU holds one (the ring
+// fills its LDS).  A split adds a launch, 0.45 us per range (one thread
+// adds them in turn) and its partial sums at 4.8 TB/s.
+// Fitted to 45 blocks, 24 x 30 x 161 to 1024 x 12288 x 4096, each product
+// timed with both tiles in 1 to 16 ranges; by it the choice is 1% slower than
+// the fastest of them in the mean, 4.5 us at worst.  (256 x 192, 128 x 256 and
+// 128 x 192 tiles were built and timed too: the best in 6 of 73 products, by
+// 10% at most, and are gone.)
+Grid grid_of(int num_cu, BlockForm form, const BlockArgs& a, int size, int requested) {
     const bool dual = form == mgemm::BLOCK_FORWARD || form == mgemm::BLOCK_AGAIN;
-    const mgemm_host::GatedTile& forced = h->gated_tile[dual ? 0 : form == mgemm::BLOCK_DX ? 1 : 2];
-    BlockTile best{0, 0, 0};
-    double best_t = 1e300;
-    for (int bm : {256, 128})
-        for (int bn : {256, 192, 128}) {
-            if (!mgemm::block_has(form, bm, bn)) continue;
-            if (forced.rows != 0 && (forced.rows != bm || forced.columns != bn)) continue;
-            const int out = dual ? bn / 2 : bn;
-            const int64_t slices = a.K / mgemm::slice_of(bm) * (form == mgemm::BLOCK_DX ? 2 : 1);
-            Problem q{};
-            q.M = up(a.M, bm) * a.batches_m;
-            q.N = up(a.N, out) * a.batches_n;
-            q.K = a.K * (form == mgemm::BLOCK_DX ? 2 : 1);
-            q.num_cu = h->num_cu;
-            for (int req = 1, last = 0; req <= mgemm::MAX_KSPLIT; ++req) {
-                if (forced.rows != 0 && forced.ksplit != 0 && req != forced.ksplit) continue;
-                const BlockTile t{bm, bn, mgemm::block_splits(slices, req)};
-                if (t.ks <= last) continue;
-                last = t.ks;
-                if (t.ks > 1 && mgemm::block_part_bytes(form, a, t) > h->ws.part_bytes) break;
-                const double us = predict_us(q, bm, bn, out, bn == 256 ? 1.4 : 1.3, 1, t.ks);
-                if (us < best_t) { best_t = us; best = t; }
-            }
+    const int out = dual ? size / 2 : size, slice = mgemm::slice_of(size);
+    const int64_t cus = num_cu > 0 ? num_cu : 256;
+    const int64_t slices = a.K / slice * (form == mgemm::BLOCK_DX ? 2 : 1);
+    Grid g{};
+    g.tile = BlockTile{size, mgemm::block_splits(slices, requested)};
+    g.tiles = (a.M + size - 1) / size * a.batches_m * ((a.N + out - 1) / out * a.batches_n);
+    g.wgs = g.tiles * g.tile.ks;
+    const int64_t per = (slices + g.tile.ks - 1) / g.tile.ks;
+    g.wg_us = (double)per * slice / 64 * (size == 256 ? 1.45 : 0.45) + (size == 256 ? 7.0 : 3.6);
+    if (g.tile.ks > 1) {
+        g.part_bytes = g.wgs * size * size * 4;
+        g.sum_us = 3.0 + 0.45 * g.tile.ks + (double)g.part_bytes / 4.8e6;
+    }
+    // Few rounds of workgroups end together; many even out.
+    const double rounds = g.wgs <= 4 * cus ? (double)((g.wgs + cus - 1) / cus) : (double)g.wgs / cus;
+    g.us = rounds * g.wg_us + g.sum_us;
+    return g;
+}
+
+// The grids that a product may run as (those of its forced tile), a few splits
+// of each size: the choice is made in every call, on the host.
+struct Grids {
+    Grid g[2 * 12];
+    int n = 0;
+};
+Grids grids_of(mgemm_handle_t h, BlockForm form, const BlockArgs& a) {
+    static constexpr int SPLITS[12] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32};
+    const auto& forced = h->gated_tile[form == mgemm::BLOCK_DX ? 1 : form == mgemm::BLOCK_DW ? 2 : 0];
+    Grids out;
+    for (int size : {256, 128}) {
+        if (forced.size != 0 && forced.size != size) continue;
+        int last = 0;
+        for (int req : SPLITS) {
+            if (forced.ksplit != 0) req = forced.ksplit;
+            const Grid g = grid_of(h->num_cu, form, a, size, req);
+            if (g.tile.ks <= last) continue;
+            last = g.tile.ks;
+            if (g.part_bytes <= h->ws.part_bytes) out.g[out.n++] = g;
         }
+    }
+    return out;
+}
+
+// The fastest by prediction; wgs 0: none fits the workspace (a forced split).
+Grid fastest(const Grids& all) {
+    Grid best{};
+    for (int i = 0; i < all.n; ++i)
+        if (best.wgs == 0 || all.g[i].us < best.us) best = all.g[i];
     return best;
 }
 
-// Whether dX and the weights' gradients run as one launch of 128x128 tiles;
-// then xt and wt become its splits.
-bool choose_pair(mgemm_handle_t h, const BlockArgs& x, const BlockArgs& w, BlockTile& xt, BlockTile& wt) {
-    const auto &fx = h->gated_tile[1], &fw = h->gated_tile[2];
+// Whether dX and the weights' gradients run as one launch of 128 tiles, and
+// then in which splits: where both together fill the CUs at most twice, the
+// launch lasts as long as the longer of its workgroups and not as the sum of
+// two launches (333 x 1004 x 515 FP16 computed again: 31.8 us against 37.6).
+bool choose_pair(mgemm_handle_t h, const Grids& x, const Grids& w, Grid& xg, Grid& wg) {
     const int64_t cus = h->num_cu > 0 ? h->num_cu : 256;
-    const BlockTile one{128, 128, 1};
-    const int64_t nx = mgemm::block_tiles(mgemm::BLOCK_DX, x, one), nw = mgemm::block_tiles(mgemm::BLOCK_DW, w, one);
-    auto small = [](const BlockTile& t) { return t.bm == 128 && t.bn == 128; };
-    if (fx.rows != 0 || fw.rows != 0)
-        return small(xt) && small(wt) && nx * xt.ks + nw * wt.ks <= 2 * cus &&
-               mgemm::block_part_bytes(mgemm::BLOCK_DX, x, xt) + mgemm::block_part_bytes(mgemm::BLOCK_DW, w, wt) <=
-                   h->ws.part_bytes;
-    return small(xt) && small(wt) && nx + nw <= cus && xt.ks == 1 && wt.ks == 1;
+    double best = xg.us + wg.us;
+    bool pair = false;
+    for (int i = 0; i < x.n; ++i) {
+        const Grid& a = x.g[i];
+        if (a.tile.size != 128 || a.wgs > 2 * cus) continue;
+        for (int j = 0; j < w.n; ++j) {
+            const Grid& b = w.g[j];
+            if (b.tile.size != 128 || a.wgs + b.wgs > 2 * cus || a.part_bytes + b.part_bytes > h->ws.part_bytes)
+                continue;
+            const double longer = a.wg_us > b.wg_us ? a.wg_us : b.wg_us;
+            const double shared = (a.wgs * a.wg_us + b.wgs * b.wg_us) / cus + (a.wgs + b.wgs > cus ? longer / 2 : 0.0);
+            const double us = (longer > shared ? longer : shared) + (a.sum_us > b.sum_us ? a.sum_us : b.sum_us);
+            if (us < best) {
+                best = us;
+                pair = true;
+                xg = a;
+                wg = b;
+            }
+        }
+    }
+    return pair;
 }
 
 // Whether the grids and slice counts of these sizes stay within 32 bits.
@@ -214,24 +270,10 @@ mgemm_status_t check_work(const Plan& p, void* work, int64_t bytes, char** out) 
 
 namespace mgemm {
 
-bool block_has(BlockForm f, int bm, int bn) {
-    if (bm == 256) return bn == 256 || bn == 192;
-    return bm == 128 && (bn == 128 || bn == (f == BLOCK_FORWARD || f == BLOCK_AGAIN ? 256 : 192));
-}
-
 int block_splits(int64_t slices, int requested) {
     if (requested <= 1 || slices < 2) return 1;
     const int64_t ks = requested < slices ? requested : slices, nks = (slices + ks - 1) / ks;
     return (int)((slices + nks - 1) / nks);
-}
-
-int64_t block_tiles(BlockForm f, const BlockArgs& a, BlockTile t) {
-    const int out = f == BLOCK_FORWARD || f == BLOCK_AGAIN ? t.bn / 2 : t.bn;
-    return (a.M + t.bm - 1) / t.bm * a.batches_m * ((a.N + out - 1) / out * a.batches_n);
-}
-
-int64_t block_part_bytes(BlockForm f, const BlockArgs& a, BlockTile t) {
-    return block_tiles(f, a, t) * t.ks * t.bm * t.bn * 4;
 }
 
 }  // namespace mgemm
@@ -251,16 +293,10 @@ mgemm_status_t mgemm_gated_workspace(mgemm_layout_t layoutW, int64_t M, int64_t 
     return MGEMM_SUCCESS;
 }
 
-mgemm_status_t mgemm_set_gated_tile(mgemm_handle_t h, int32_t product, int32_t rows, int32_t columns,
-                                    int32_t ksplit) {
+mgemm_status_t mgemm_set_gated_tile(mgemm_handle_t h, int32_t product, int32_t size, int32_t ksplit) {
     if (!h || product < 0 || product > 2 || ksplit < 0 || ksplit > MGEMM_MAX_KSPLIT) return MGEMM_ERR_INVALID_ARG;
-    if (rows != 0) {
-        const BlockForm f = product == 0 ? mgemm::BLOCK_FORWARD : product == 1 ? mgemm::BLOCK_DX : mgemm::BLOCK_DW;
-        if (!mgemm::block_has(f, rows, columns)) return MGEMM_ERR_UNSUPPORTED;
-    } else if (columns != 0 || ksplit != 0) {
-        return MGEMM_ERR_INVALID_ARG;
-    }
-    h->gated_tile[product] = mgemm_host::GatedTile{rows, columns, ksplit};
+    if (size != 0 && size != 128 && size != 256) return MGEMM_ERR_INVALID_ARG;
+    h->gated_tile[product] = mgemm_host::GatedTile{size, ksplit};
     return MGEMM_SUCCESS;
 }
 
@@ -286,15 +322,15 @@ mgemm_status_t mgemm_gated_forward(mgemm_handle_t h, mgemm_layout_t layoutW, int
     char* w;
     if (const mgemm_status_t st = check_work(p, work, work_bytes, &w); st != MGEMM_SUCCESS) return st;
     BlockArgs a = base_args(h->ws, M, N, p.copy_x && p.copy_w ? up(K, SLICE) : K);
-    const BlockTile t = choose(h, mgemm::BLOCK_FORWARD, a);
-    if (t.ks < 1) return MGEMM_ERR_UNSUPPORTED;
+    const Grid g = fastest(grids_of(h, mgemm::BLOCK_FORWARD, a));
+    if (g.wgs == 0) return MGEMM_ERR_UNSUPPORTED;
     Operands o{X, Wg, Wu, ldx, ldw};
     if (const mgemm_status_t st = lay_out(p, w, o, stream); st != MGEMM_SUCCESS) return st;
     a.A[0] = a.A[1] = o.X; a.lda = o.ldx;
     a.B[0] = o.Wg; a.B[1] = o.Wu; a.ldb = o.ldw;
     a.Z = Z; a.ldz = ldz;
     a.C[0] = G; a.C[1] = U; a.ldc = ldg;
-    return status(mgemm::launch_block_forward(a, (int)dtype, p.col, false, t, stream));
+    return status(mgemm::launch_block_forward(a, (int)dtype, p.col, false, g.tile, stream));
 }
 
 mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, int64_t M, int64_t N, int64_t K,
@@ -328,13 +364,13 @@ mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, in
     BlockArgs fa = base_args(h->ws, Mp, Np, p.copy_x && p.copy_w ? up(K, SLICE) : K), xa = base_args(h->ws, M, K, Np),
               wa = col ? base_args(h->ws, N, K, Mp) : base_args(h->ws, K, N, Mp);
     (col ? wa.batches_m : wa.batches_n) = 2;
-    const BlockTile ft = again ? choose(h, mgemm::BLOCK_AGAIN, fa) : BlockTile{0, 0, 1};
-    BlockTile xt{0, 0, 1}, wt{0, 0, 1};
-    bool pair = false;
-    if (dX) xt = choose(h, mgemm::BLOCK_DX, xa);
-    if (dWg) wt = choose(h, mgemm::BLOCK_DW, wa);
-    if (dX && dWg) pair = choose_pair(h, xa, wa, xt, wt);
-    if (ft.ks < 1 || xt.ks < 1 || wt.ks < 1) return MGEMM_ERR_UNSUPPORTED;
+    Grid fg{}, xg{}, wg{};
+    Grids xs, ws;
+    if (again) fg = fastest(grids_of(h, mgemm::BLOCK_AGAIN, fa));
+    if (dX) xg = fastest(xs = grids_of(h, mgemm::BLOCK_DX, xa));
+    if (dWg) wg = fastest(ws = grids_of(h, mgemm::BLOCK_DW, wa));
+    if ((again && fg.wgs == 0) || (dX && xg.wgs == 0) || (dWg && wg.wgs == 0)) return MGEMM_ERR_UNSUPPORTED;
+    const bool pair = dX && dWg && choose_pair(h, xs, ws, xg, wg);
     Operands o{X, Wg, Wu, ldx, ldw};
     if (const mgemm_status_t st = lay_out(p, w, o, stream); st != MGEMM_SUCCESS) return st;
     void *dG = w + p.dg_at, *dU = w + p.du_at;
@@ -346,7 +382,7 @@ mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, in
         fa.dZ = dZ; fa.ldz = lddz;
         fa.Mz = M; fa.Nz = N;
         fa.C[0] = dG; fa.C[1] = dU; fa.ldc = ldd;
-        e = mgemm::launch_block_forward(fa, (int)dtype, col, true, ft, stream);
+        e = mgemm::launch_block_forward(fa, (int)dtype, col, true, fg.tile, stream);
     } else {
         e = mgemm::launch_gated_grad(M, N, p.d_rows, p.d_cols, G, U, ldg, dZ, lddz, dG, dU, ldd, (int)dtype, stream);
     }
@@ -368,9 +404,9 @@ mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, in
     wa.ldc = lddw;
     wa.beta = beta;
     // Row-major weights (in x out) are contiguous along dX's contraction.
-    if (pair) return status(mgemm::launch_block_pair(xa, wa, (int)dtype, !col, xt.ks, wt.ks, stream));
-    if (dX) e = mgemm::launch_block_dx(xa, (int)dtype, !col, xt, stream);
-    if (dWg && e == hipSuccess) e = mgemm::launch_block_dw(wa, (int)dtype, wt, stream);
+    if (pair) return status(mgemm::launch_block_pair(xa, wa, (int)dtype, !col, xg.tile.ks, wg.tile.ks, stream));
+    if (dX) e = mgemm::launch_block_dx(xa, (int)dtype, !col, xg.tile, stream);
+    if (dWg && e == hipSuccess) e = mgemm::launch_block_dw(wa, (int)dtype, wg.tile, stream);
     return status(e);
 }
 

@@ -5,9 +5,8 @@
 // MFMAs pinned so that one wave per SIMD keeps its matrix core fed: the
 // schedule and LDS layouts of k_h_dma.hip.  What differs is how operands are
 // found:
-//   forward  one A (X) against the two weights in one tile, 96 columns of
-//            each, so that a lane holds G and U of the same outputs and X is
-//            read once;
+//   forward  one A (X) against the two weights in one tile, so that a lane
+//            holds G and U of the same outputs and X is read once;
 //   dX       the contraction runs over two segments (dG with Wg, then dU with
 //            Wu) into one accumulator: no second pass over dX, one rounding;
 //   dW       both gradients in one grid: a tile's batch picks its matrices.
@@ -35,18 +34,18 @@ constexpr int LDS_MAX = 160 * 1024;
 template <int FORM>
 constexpr bool is_dual() { return FORM == BLOCK_FORWARD || FORM == BLOCK_AGAIN; }
 
-// Waves are 2x2.  A forward tile's B slot holds BN/2 columns of Wg, then the
-// same BN/2 of Wu; a wave takes the same columns of both, so that G and U of
-// an output are in matching registers of one lane.  With BN = 192 the 96
-// columns of each do not halve into 32-column blocks: waves are then 4x1, a
-// wave holds BM/4 rows of all of them.
-template <int FORM, int BM_, int BN_>
+// Square tiles, waves 2x2.  A forward tile's B slot holds T/2 columns of Wg,
+// then the same T/2 of Wu; a wave takes the same columns of both, so that G
+// and U of an output are in matching registers of one lane.
+template <int FORM, int T>
 struct Cfg {
     static constexpr bool DUAL = is_dual<FORM>();
-    static constexpr int BM = BM_, BN = BN_;
-    static_assert(BN == 256 || BN == 192 || BN == 128, "tile width");
-    static_assert(BM == 256 || BM == 128, "tile height");
-    static constexpr bool TALL = DUAL && BN == 192;                  // waves 4x1
+    static constexpr int BM = T, BN = T;
+    static_assert(T == 256 || T == 128, "tile size");
+    // A slice of 64 is a 128-byte line of a K-contiguous row.  With 32 each
+    // line is fetched twice, half of it used (128 x 128 tiles, both operands
+    // K-contiguous: 0.31 us per 32 against 0.20); the 256 tile's ring has no
+    // room for more than two slices of 64.
     static constexpr int BK = slice_of(BM), KS = BK / 16;            // elements and K-steps of a slice
     static constexpr int ROW = BK * 2;                               // bytes of a K-contiguous row of a slice
     static constexpr int A_BYTES = BM * ROW, A_COPIES = A_BYTES / 4096;   // 1 KiB copies per wave per slice
@@ -55,21 +54,19 @@ struct Cfg {
     static constexpr int COPIES = A_COPIES + B_COPIES;
     static constexpr int SLOT_BYTES = A_BYTES + B_BYTES;
     // As many slices in flight as fit: all workgroups of an XCD walk the
-    // contraction together, so each slice's first request goes to memory
-    // (1 to 2 us under load), and a small tile's slice lasts 0.2 us.
-    static constexpr int SLOTS = LDS_MAX / SLOT_BYTES < 8 ? LDS_MAX / SLOT_BYTES : 8, AHEAD = SLOTS - 1;
-    static constexpr int WROWS = TALL ? BM / 4 : BM / 2;
-    static constexpr int TM = WROWS / 32, TN = TALL ? BN / 32 : BN / 64;
+    // contraction together, so each slice's first request goes to memory (1 to
+    // 2 us under load).
+    static constexpr int SLOTS = LDS_MAX / SLOT_BYTES, AHEAD = SLOTS - 1;
+    static constexpr int WROWS = BM / 2, TM = WROWS / 32, TN = BN / 64;
     static constexpr int OUT = DUAL ? BN / 2 : BN;                   // output columns of a tile
-    static constexpr int WOUT = TALL ? OUT : OUT / 2;                // of a wave
+    static constexpr int WOUT = OUT / 2;                             // of a wave
     static constexpr int TNO = DUAL ? TN / 2 : TN;                   // 32-column output blocks of a wave
     static constexpr int STAGE_ROW = WOUT * 2 + 16;                  // bytes of a staged row of outputs
     static constexpr int LDS = SLOTS * SLOT_BYTES;
     static_assert(4 * 3 * 32 * STAGE_ROW <= LDS, "outputs are staged in the ring");
     // Slot column of a wave's 32-column block t.
     static __device__ __forceinline__ int column(int wn, int t) {
-        if constexpr (TALL) return 32 * t;
-        else if constexpr (DUAL) return (t < TNO ? 0 : OUT) + WOUT * wn + 32 * (t % TNO);
+        if constexpr (DUAL) return (t < TNO ? 0 : OUT) + WOUT * wn + 32 * (t % TNO);
         else return WOUT * wn + 32 * t;
     }
 };
@@ -81,13 +78,9 @@ __device__ __forceinline__ int row_swz(int r) {
     if constexpr (BK == 64) return (r >> 1) & 7;
     else return ((r >> 1) ^ (r >> 2)) & 3;
 }
-// Chunk position of chunk c in K-row k of a slot whose K-rows are W elements
-// wide (an involution for each k): free of bank conflicts for the transposed reads.
-template <int W>
-__device__ __forceinline__ int chunk_pos(int c, int k) {
-    if constexpr (W == 192) return (c & ~7) | ((c & 7) ^ (int)((0x6204035651271642ull >> ((k & 15) * 4)) & 7));
-    else return c ^ ((0xCA60 >> ((k & 3) * 4)) & 15);
-}
+// Chunk position of chunk c in K-row k of a slot whose K-rows are 128 or 256
+// elements wide: free of bank conflicts for the transposed reads.
+__device__ __forceinline__ int chunk_pos(int c, int k) { return c ^ ((0xCA60 >> ((k & 3) * 4)) & 15); }
 
 template <int DT>
 __device__ __forceinline__ f32x16 mfma(i32x4 a, i32x4 b, f32x16 c) {
@@ -222,9 +215,10 @@ __device__ __forceinline__ uint16_t* plane_of(const BlockArgs& f, int plane, int
 enum Store : int { STORE_OUT = 0, STORE_PART = 1, STORE_EITHER = 2 };
 
 // Workgroup bid of nblocks.
-template <int DT, int FORM, int BM, int BN, bool AMC, bool BKC, int STORE>
+template <int DT, int FORM, int T, bool AMC, bool BKC, int STORE>
 __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblocks, unsigned char* smem) {
-    using G = Cfg<FORM, BM, BN>;
+    using G = Cfg<FORM, T>;
+    constexpr int BM = T, BN = T;
     constexpr bool DUAL = G::DUAL;
     constexpr int SEGS = FORM == BLOCK_DX ? 2 : 1;
     static_assert(!(AMC && (BKC || DUAL)), "operand forms");
@@ -235,7 +229,7 @@ __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblo
     using Fr = Frags<TM, TN>;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = G::TALL ? wave : wave >> 1, wn = G::TALL ? 0 : wave & 1;
+    const int wm = wave >> 1, wn = wave & 1;
     const int tiles_m = (int)((f.M + BM - 1) / BM), tiles_n = (int)((f.N + G::OUT - 1) / G::OUT);
     const int pos = xcd_linear(bid, nblocks);
     const int split = pos % f.ksplit;
@@ -268,7 +262,7 @@ __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblo
     for (int i = 0; i < A_COPIES; ++i) {
         if constexpr (AMC) {
             const int j = wave * A_COPIES + i, q = 64 * j + lane, k = q / A_CHUNKS;
-            int c = chunk_pos<BM>(q % A_CHUNKS, k);
+            int c = chunk_pos(q % A_CHUNKS, k);
             const int64_t left = (f.Mr - m0) / 8 - 1;
             c = c <= left ? c : (int)left;
             src[i] = A + ((int64_t)k * f.lda + m0 + 8 * c) * 2;
@@ -292,7 +286,7 @@ __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblo
             dst[A_COPIES + i] = A_BYTES + r0 * ROW;
         } else {
             const int j = wave * G::B_COPIES + i, q = 64 * j + lane, k = q / G::B_CHUNKS;
-            int c = chunk_pos<BN>(q % G::B_CHUNKS, k);
+            int c = chunk_pos(q % G::B_CHUNKS, k);
             const bool second = DUAL && c >= G::OUT / 8;
             if (second) c -= G::OUT / 8;
             const int64_t left = (f.Nr - n0) / 8 - 1;
@@ -323,7 +317,7 @@ __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblo
                 for (int h = 0; h < 2; ++h) {
                     const int k = ks * 16 + 8 * (q4 >> 1) + 4 * h + (t16 >> 2);
                     const int m = G::WROWS * wm + 32 * t + 16 * (q4 & 1) + 4 * (t16 & 3);
-                    a_off[t][ks][h] = k * A_KROW + (chunk_pos<BM>(m >> 3, k) << 4) + ((m & 7) << 1);
+                    a_off[t][ks][h] = k * A_KROW + (chunk_pos(m >> 3, k) << 4) + ((m & 7) << 1);
                 }
             } else {
                 const int r = G::WROWS * wm + 32 * t + (lane & 31);
@@ -342,7 +336,7 @@ __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblo
                 for (int h = 0; h < 2; ++h) {
                     const int k = ks * 16 + 8 * (q4 >> 1) + 4 * h + (t16 >> 2);
                     const int n = G::column(wn, t) + 16 * (q4 & 1) + 4 * (t16 & 3);
-                    b_off[t][ks][h] = A_BYTES + k * B_ROW + (chunk_pos<BN>(n >> 3, k) << 4) + ((n & 7) << 1);
+                    b_off[t][ks][h] = A_BYTES + k * B_ROW + (chunk_pos(n >> 3, k) << 4) + ((n & 7) << 1);
                 }
             }
         }
@@ -616,21 +610,22 @@ __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblo
     }
 }
 
-template <int DT, int FORM, int BM, int BN, bool AMC, bool BKC, int STORE>
+template <int DT, int FORM, int T, bool AMC, bool BKC, int STORE>
 __global__ __launch_bounds__(NT, 1) void k_block(BlockArgs f) {
     extern __shared__ __align__(16) unsigned char smem[];
-    block_body<DT, FORM, BM, BN, AMC, BKC, STORE>(f, blockIdx.x, gridDim.x, smem);
+    block_body<DT, FORM, T, AMC, BKC, STORE>(f, blockIdx.x, gridDim.x, smem);
 }
 
 // Second phase of a split: one thread per 16-byte chunk of a tile's
 // accumulators sums the ranges in range order and stores four outputs.
-template <int DT, int FORM, int BM, int BN>
+template <int DT, int FORM, int T>
 __device__ __forceinline__ void reduce_body(const BlockArgs& f, int bid, int nblocks) {
-    using G = Cfg<FORM, BM, BN>;
+    using G = Cfg<FORM, T>;
+    constexpr int BM = T;
     constexpr int TM = G::TM, TN = G::TN, TNO = G::TNO, CH = TM * TNO * 4;
     constexpr int64_t TILE = (int64_t)NT * TM * TN * 16;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = G::TALL ? wave : wave >> 1, wn = G::TALL ? 0 : wave & 1;
+    const int wm = wave >> 1, wn = wave & 1;
     const int tiles_m = (int)((f.M + BM - 1) / BM), tiles_n = (int)((f.N + G::OUT - 1) / G::OUT);
     const int pos = xcd_linear(bid, nblocks);
     const int c = pos % CH;
@@ -650,13 +645,15 @@ __device__ __forceinline__ void reduce_body(const BlockArgs& f, int bid, int nbl
     auto sum = [&](int chunk) {
         const float* p = part + (int64_t)chunk * NT * 4;
         f32x4 a = *(const f32x4*)p;
-        int s = 1;
-        for (; s + 4 <= f.ksplit; s += 4) {
-            const f32x4 b0 = *(const f32x4*)(p + s * TILE), b1 = *(const f32x4*)(p + (s + 1) * TILE);
-            const f32x4 b2 = *(const f32x4*)(p + (s + 2) * TILE), b3 = *(const f32x4*)(p + (s + 3) * TILE);
-            a = (((a + b0) + b1) + b2) + b3;
+        // Eight ranges are requested at a time and added one by one.
+        for (int s = 1; s < f.ksplit; s += 8) {
+            f32x4 b[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = s + i < f.ksplit ? *(const f32x4*)(p + (s + i) * TILE) : f32x4{};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (s + i < f.ksplit) a = a + b[i];
         }
-        for (; s < f.ksplit; ++s) a = a + *(const f32x4*)(p + s * TILE);
         return a;
     };
     f32x4 g = sum((tm * TN + tn) * 4 + q);
@@ -685,31 +682,31 @@ __device__ __forceinline__ void reduce_body(const BlockArgs& f, int bid, int nbl
     }
 }
 
-template <int DT, int FORM, int BM, int BN>
+template <int DT, int FORM, int T>
 __global__ __launch_bounds__(NT) void k_block_reduce(BlockArgs f) {
-    reduce_body<DT, FORM, BM, BN>(f, blockIdx.x, gridDim.x);
+    reduce_body<DT, FORM, T>(f, blockIdx.x, gridDim.x);
 }
 
 // Fills in the ranges and returns the workgroups of a launch with ks of them.
-template <int FORM, int BM, int BN>
+template <int FORM, int T>
 int64_t set_ranges(BlockArgs& a, int ks) {
-    using G = Cfg<FORM, BM, BN>;
+    using G = Cfg<FORM, T>;
     const int64_t slices = (a.K / G::BK) * (FORM == BLOCK_DX ? 2 : 1);
     a.nks = (int)(ks > 1 ? (slices + ks - 1) / ks : (slices > 0 ? slices : 1));
     a.ksplit = ks > 1 ? (int)((slices + a.nks - 1) / a.nks) : 1;
-    return ((a.M + BM - 1) / BM) * a.batches_m * (((a.N + G::OUT - 1) / G::OUT) * a.batches_n) * a.ksplit;
+    return ((a.M + T - 1) / T) * a.batches_m * (((a.N + G::OUT - 1) / G::OUT) * a.batches_n) * a.ksplit;
 }
 // Workgroups of the second phase, per tile.
-template <int FORM, int BM, int BN>
+template <int FORM, int T>
 constexpr int reduce_chunks() {
-    using G = Cfg<FORM, BM, BN>;
+    using G = Cfg<FORM, T>;
     return G::TM * G::TNO * 4;
 }
 
-template <int DT, int FORM, int BM, int BN, bool AMC, bool BKC>
+template <int DT, int FORM, int T, bool AMC, bool BKC>
 hipError_t launch_block(BlockArgs a, int ks, hipStream_t s) {
-    using G = Cfg<FORM, BM, BN>;
-    const int64_t wgs = set_ranges<FORM, BM, BN>(a, ks);
+    using G = Cfg<FORM, T>;
+    const int64_t wgs = set_ranges<FORM, T>(a, ks);
     auto go = [&](auto kern, bool (&done)[MAX_DEVICES]) -> hipError_t {
         if (hipError_t e = set_lds_limit_once((const void*)kern, G::LDS, done); e != hipSuccess) return e;
         hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(NT), G::LDS, s, a);
@@ -717,12 +714,12 @@ hipError_t launch_block(BlockArgs a, int ks, hipStream_t s) {
     };
     if (a.ksplit == 1) {
         static bool done[MAX_DEVICES] = {};
-        return go(k_block<DT, FORM, BM, BN, AMC, BKC, STORE_OUT>, done);
+        return go(k_block<DT, FORM, T, AMC, BKC, STORE_OUT>, done);
     }
     static bool done[MAX_DEVICES] = {};
-    if (hipError_t e = go(k_block<DT, FORM, BM, BN, AMC, BKC, STORE_PART>, done); e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_block_reduce<DT, FORM, BM, BN>),
-                       dim3((unsigned)(wgs / a.ksplit * reduce_chunks<FORM, BM, BN>())), dim3(NT), 0, s, a);
+    if (hipError_t e = go(k_block<DT, FORM, T, AMC, BKC, STORE_PART>, done); e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_block_reduce<DT, FORM, T>),
+                       dim3((unsigned)(wgs / a.ksplit * reduce_chunks<FORM, T>())), dim3(NT), 0, s, a);
     return hipGetLastError();
 }
 

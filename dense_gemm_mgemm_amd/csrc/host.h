@@ -36,9 +36,10 @@ struct Table {
     std::map<TableKey, TableEntry> entries;
 };
 
-// A tile forced on a product of the gated block (mgemm_set_gated_tile); rows 0: none.
+// A tile size and split forced on a product of the gated block
+// (mgemm_set_gated_tile); 0: the library's choice.
 struct GatedTile {
-    int rows, columns, ksplit;
+    int size, ksplit;
 };
 
 TableKey exact_key(const Problem& p);

@@ -7,11 +7,8 @@ namespace {
 
 template <int DT>
 hipError_t by_tile(const BlockArgs& a, BlockTile t, hipStream_t s) {
-    if (t.bm == 128)
-        return t.bn == 128 ? launch_block<DT, BLOCK_DW, 128, 128, true, false>(a, t.ks, s)
-                           : launch_block<DT, BLOCK_DW, 128, 192, true, false>(a, t.ks, s);
-    return t.bn == 192 ? launch_block<DT, BLOCK_DW, 256, 192, true, false>(a, t.ks, s)
-                       : launch_block<DT, BLOCK_DW, 256, 256, true, false>(a, t.ks, s);
+    return t.size == 128 ? launch_block<DT, BLOCK_DW, 128, true, false>(a, t.ks, s)
+                         : launch_block<DT, BLOCK_DW, 256, true, false>(a, t.ks, s);
 }
 
 }  // namespace

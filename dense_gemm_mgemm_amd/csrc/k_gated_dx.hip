@@ -6,11 +6,8 @@ namespace {
 
 template <int DT, bool BKC>
 hipError_t by_tile(const BlockArgs& a, BlockTile t, hipStream_t s) {
-    if (t.bm == 128)
-        return t.bn == 128 ? launch_block<DT, BLOCK_DX, 128, 128, false, BKC>(a, t.ks, s)
-                           : launch_block<DT, BLOCK_DX, 128, 192, false, BKC>(a, t.ks, s);
-    return t.bn == 192 ? launch_block<DT, BLOCK_DX, 256, 192, false, BKC>(a, t.ks, s)
-                       : launch_block<DT, BLOCK_DX, 256, 256, false, BKC>(a, t.ks, s);
+    return t.size == 128 ? launch_block<DT, BLOCK_DX, 128, false, BKC>(a, t.ks, s)
+                         : launch_block<DT, BLOCK_DX, 256, false, BKC>(a, t.ks, s);
 }
 
 }  // namespace

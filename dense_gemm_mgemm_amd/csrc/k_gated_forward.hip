@@ -8,11 +8,8 @@ namespace {
 
 template <int DT, int FORM, bool BKC>
 hipError_t by_tile(const BlockArgs& a, BlockTile t, hipStream_t s) {
-    if (t.bm == 128)
-        return t.bn == 128 ? launch_block<DT, FORM, 128, 128, false, BKC>(a, t.ks, s)
-                           : launch_block<DT, FORM, 128, 256, false, BKC>(a, t.ks, s);
-    return t.bn == 192 ? launch_block<DT, FORM, 256, 192, false, BKC>(a, t.ks, s)
-                       : launch_block<DT, FORM, 256, 256, false, BKC>(a, t.ks, s);
+    return t.size == 128 ? launch_block<DT, FORM, 128, false, BKC>(a, t.ks, s)
+                         : launch_block<DT, FORM, 256, false, BKC>(a, t.ks, s);
 }
 template <int DT, int FORM>
 hipError_t by_layout(const BlockArgs& a, bool b_kc, BlockTile t, hipStream_t s) {

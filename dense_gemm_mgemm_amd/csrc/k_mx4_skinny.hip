@@ -1,13 +1,13 @@
 // Microscaled 4-bit products for few rows (M <= 64): a stream of the weights.
 //
 // A workgroup of eight waves owns 16 * NTW output columns and all of K; wave
-// w takes the 128-element slices w, w + 8, ... of every row, so that the eight
-// waves together read 512 consecutive bytes of each weight row at a time, and
-// the waves' FP32 sums are added in wave order through LDS: the result does
-// not depend on timing and there is no second launch.  Weights go from memory
+// w takes the steps w, w + 8, ... of one or two adjacent 128-element slices (a
+// 128-byte line) of every row, and the waves' FP32 sums are added in wave order
+// through LDS: the result does not depend on timing and there is no second
+// launch.  Weights go from memory
 // to registers: lane l of v_mfma_scale_f32_16x16x128_f8f6f4 holds block l/16
 // of row l%16, which is one 16-byte load, and its scale is one byte of
-// the row's dword of four.  The next step's slices are requested before
+// the slice's dword of four.  The next step's slices are requested before
 // the present ones are multiplied.
 //
 // M <= 16: the activations are quantised here (RM rows at most, as 16-byte
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(NT) void k_mx4_skinny(Problem p, Mx4Args f) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * (16 * NTW);
     const int blocks = (int)((p.K + MX_BLOCK - 1) / MX_BLOCK);
-    const int slices = (blocks + 3) / 4;
+    const int steps = (blocks + 4 * U - 1) / (4 * U);     // U adjacent slices each
     const int lr = lane & 15, lc = lane >> 4;             // this lane's row of a tile and block of a slice
 
     const uint8_t* w[NTW * NB];
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(NT) void k_mx4_skinny(Problem p, Mx4Args f) {
         int64_t n = n0 + 16 * (t / NB) + lr;
         n = n < p.N ? n : p.N - 1;
         w[t] = (const uint8_t*)(t % NB ? p.B2 : p.B) + n * p.ldb + 16 * lc;
-        ws[t] = (t % NB ? f.sb2 : f.sb) + n * f.ldsb + lc;
+        ws[t] = (t % NB ? f.sb2 : f.sb) + n * f.ldsb;
     }
     const uint8_t* a[MT];
     const uint8_t* as[MT];
@@ -76,43 +76,29 @@ __global__ __launch_bounds__(NT) void k_mx4_skinny(Problem p, Mx4Args f) {
             int64_t m = 16 * t + lr;
             m = m < p.M ? m : p.M - 1;
             a[t] = (const uint8_t*)p.A + m * p.lda + 16 * lc;
-            as[t] = f.sa + m * f.ldsa + lc;
+            as[t] = f.sa + m * f.ldsa;
         }
     }
+    typedef unsigned Sc __attribute__((ext_vector_type(U)));
     struct Step {
+        u32x4 x[CL][XT == F32 ? 2 : 1];
         i32x4 w[U][NTW * NB];
         int ws[U][NTW * NB];
         i32x4 a[U][QX ? 1 : MT];
         int as[U][QX ? 1 : MT];
-        u32x4 x[CL][XT == F32 ? 2 : 1];
     };
-    // Requests the slices s, s + NW, .. of one step; blocks past K read as
-    // zero codes with scale 1.
-    auto request = [&](Step& st, int s) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int sl = s + u * NW;
-            const bool in = 4 * sl + lc < blocks;
-#pragma unroll
-            for (int t = 0; t < NTW * NB; ++t) {
-                st.w[u][t] = in ? *(const i32x4*)(w[t] + (int64_t)sl * 64) : i32x4{0, 0, 0, 0};
-                st.ws[u][t] = in ? (int)ws[t][(int64_t)sl * 4] : 127;
-            }
-            if constexpr (!QX) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    st.a[u][t] = in ? *(const i32x4*)(a[t] + (int64_t)sl * 64) : i32x4{0, 0, 0, 0};
-                    st.as[u][t] = in ? (int)as[t][(int64_t)sl * 4] : 127;
-                }
-            }
-        }
+    // Requests step q: the activations first (they come from L2, are waited for
+    // first and are quantised while the weights are still on their way), then
+    // a row's codes and the scales of its U slices in one load.  Blocks past K
+    // read as zero codes with scale 1.
+    auto request = [&](Step& st, int q) {
         if constexpr (QX) {
             // Chunk c = 64 i + lane of the step: slice c / (16 RM), row
             // (c / 16) % RM, elements 8 (c % 16) of the slice.
 #pragma unroll
             for (int i = 0; i < CL; ++i) {
                 const int c = 64 * i + lane, m = (c >> 4) % RM;
-                const int64_t k = (int64_t)(s + c / (16 * RM) * NW) * 128 + 8 * (c & 15);
+                const int64_t k = (int64_t)(U * q + c / (16 * RM)) * 128 + 8 * (c & 15);
                 const unsigned char* x = (const unsigned char*)f.X + (m * f.ldx + k) * XS;
                 u32x4 v[2] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
                 if (m < p.M && k + 8 <= p.K) {
@@ -129,6 +115,24 @@ __global__ __launch_bounds__(NT) void k_mx4_skinny(Problem p, Mx4Args f) {
                 st.x[i][0] = v[0];
                 if constexpr (XT == F32) st.x[i][1] = v[1];
             }
+        }
+        auto row = [&](const uint8_t* codes, const uint8_t* scales, i32x4* c0, int* s0, int stride) {
+            Sc sc;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool in = 4 * (U * q + u) + lc < blocks;
+                c0[u * stride] = in ? *(const i32x4*)(codes + (int64_t)(U * q + u) * 64) : i32x4{0, 0, 0, 0};
+            }
+            sc = q < steps ? *(const Sc*)(scales + (int64_t)q * (4 * U)) : Sc{};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                s0[u * stride] = 4 * (U * q + u) + lc < blocks ? (int)(sc[u] >> (8 * lc)) : 127;
+        };
+#pragma unroll
+        for (int t = 0; t < NTW * NB; ++t) row(w[t], ws[t], &st.w[0][t], &st.ws[0][t], NTW * NB);
+        if constexpr (!QX) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) row(a[t], as[t], &st.a[0][t], &st.as[0][t], MT);
         }
     };
 
@@ -198,10 +202,10 @@ __global__ __launch_bounds__(NT) void k_mx4_skinny(Problem p, Mx4Args f) {
 
     Step s0, s1;
     request(s0, wave);
-    for (int s = wave; s < slices; s += 2 * U * NW) {
-        request(s1, s + U * NW);
+    for (int q = wave; q < steps; q += 2 * NW) {
+        request(s1, q + NW);
         multiply(s0);
-        request(s0, s + 2 * U * NW);
+        request(s0, q + 2 * NW);
         multiply(s1);
     }
 
@@ -280,6 +284,10 @@ bool mx4_skinny_supports(const Problem& p, const Mx4Args& a) {
     auto al = [](const void* q) { return ((uintptr_t)q & 15) == 0; };
     if (p.M > (a.X != nullptr ? 16 : 64)) return false;
     if (p.ldb % 16 != 0 || !al(p.B) || !al(p.B2)) return false;
+    // A step's scales are one load of up to eight bytes.
+    auto al8 = [](const void* q) { return ((uintptr_t)q & 7) == 0; };
+    if (a.ldsb % 8 != 0 || !al8(a.sb) || !al8(a.sb2)) return false;
+    if (a.X == nullptr && (a.ldsa % 8 != 0 || !al8(a.sa))) return false;
     if (a.X != nullptr) {
         const int es = a.xtype == F32 ? 4 : 2;
         if (a.ldx * es % 16 != 0 || !al(a.X)) return false;

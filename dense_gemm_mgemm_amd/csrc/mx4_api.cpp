@@ -56,6 +56,16 @@ constexpr Shape SHAPES[] = {{MGEMM_KERNEL_MX4_MFMA, 256, 256},
                             {MGEMM_KERNEL_MX4_MFMA_128, 192, 128},
                             {MGEMM_KERNEL_MX4_MFMA_64, 192, 64}};
 
+// A tile's rate in the time model.  Few rows stream the weights from HBM: a
+// slice of the 64-row tile then takes 0.5 us whatever it computes and of the
+// 128-row tile 0.58 (48 x 4096 x 12288 in 8 ranges 14.6 and 16.8 us; 48 x 12288
+// x 4096 whole 18.4, in 4 ranges 12.9), more than their matrix time.
+double tile_speed(const Problem& p, int bn, int bm) {
+    if (bm == 64) return 0.37;
+    if (bm == 128 && p.M <= 128) return 0.63;
+    return bn == 256 ? 1.4 : 1.3;
+}
+
 // The split with the smallest predicted time for one tile shape.  A
 // 128-element slice moves the bytes and takes the matrix time of a 32-element
 // slice of a 16-bit product, so the 16-bit time model applies to K / 4, with the
@@ -70,13 +80,24 @@ Tile best_split(const Problem& p, int bn, int bm, const Workspace& ws, double* t
         const int ks = mgemm::mx4_splits(p, bn, bm, req, ws);
         if (ks <= last) continue;
         last = ks;
-        const double t = predict_us(q, bm, bn, out, bn == 256 ? 1.4 : 1.3, 1, ks, 4.5e6);
+        const double t = predict_us(q, bm, bn, out, tile_speed(p, bn, bm), 1, ks, 4.5e6);
         if (t < bt) { bt = t; best.ks = ks; }
     }
     *t_out = bt;
     return best;
 }
 
+// Predicted time (microseconds) of the decode kernel on codes: a launch, then
+// per 4096 columns (a 16-column workgroup on each CU; the gated pair has both
+// matrices') and 1024 elements of K (a slice for each wave) 0.023 us a row.
+// Measured on 4096 x 12288 weights: M = 17 / 32 / 48 / 64 12.0 / 14.3 / 20.4 /
+// 22.8 us, against 13.3 / 13.7 / 14.6 / 15.4 on 64-row tiles in 8 ranges; 12288
+// x 4096: M = 1 / 16 9.0 / 10.4 against 9.8 / 10.2 in 4; 40 x 1000 x 1000 6.0
+// against 8.0.
+double skinny_us(const Problem& p) {
+    const int64_t n = p.B2 != nullptr ? 2 * p.N : p.N;
+    return 4.5 + (double)((n + 4095) / 4096) * (double)((p.K + 1023) / 1024) * 0.023 * (double)p.M;
+}
 // Launches a product of codes: forced kernel or the library's choice.
 mgemm_status_t launch(const Problem& p, const Mx4Args& a, mgemm_kernel_t kernel, int ksplit, const Workspace& ws,
                       hipStream_t s) {
@@ -96,7 +117,8 @@ mgemm_status_t launch(const Problem& p, const Mx4Args& a, mgemm_kernel_t kernel,
         if (t < best_t) { best_t = t; best = tile; }
     }
     if (kernel == MGEMM_KERNEL_AUTO) {
-        if (p.M <= 64 && mgemm::mx4_skinny_supports(p, a)) return status(mgemm::launch_mx4_skinny(p, a, s));
+        if (mgemm::mx4_skinny_supports(p, a) && skinny_us(p) < best_t)
+            return status(mgemm::launch_mx4_skinny(p, a, s));
         if (best.bn == 0) return status(mgemm::launch_mx4_general(p, a, s));
     }
     if (best.bn == 0) return MGEMM_ERR_UNSUPPORTED;
@@ -109,7 +131,13 @@ mgemm_status_t launch(const Problem& p, const Mx4Args& a, mgemm_kernel_t kernel,
 // into the workspace a band of rows at a time.
 mgemm_status_t from_values(mgemm_handle_t h, Problem p, Mx4Args a, hipStream_t s) {
     const int es = a.xtype == mgemm::F32 ? 4 : 2, cs = p.dtype == mgemm::F32 ? 4 : 2;
-    if (mgemm::mx4_skinny_supports(p, a)) return status(mgemm::launch_mx4_skinny(p, a, s));
+    // The decode kernel's own quantisation is repeated by every workgroup and
+    // grows with the rows it has room for (4 or 16) times K: 1.6 us at 16384
+    // values (M = 1 .. 4, K = 4096: 10.6 us, from codes 9.0) and 7.6 at 65536;
+    // a launch of its own adds 2.2 (M = 8: 11.6 us, from codes 9.4).
+    constexpr int64_t IN_KERNEL = 20480;
+    if ((p.M <= 4 ? 4 : 16) * p.K <= IN_KERNEL && mgemm::mx4_skinny_supports(p, a))
+        return status(mgemm::launch_mx4_skinny(p, a, s));
     // Codes and scales take the front half of the workspace, split-K partials the rest.
     const int64_t nb = mgemm::mx4_blocks(p.K), ldq = 16 * nb, lds = (nb + 15) / 16 * 16;
     const int64_t half = h->ws.part_bytes / 2;

@@ -482,8 +482,8 @@ mgemm_status_t mgemm_run_fp8(mgemm_handle_t h, mgemm_kernel_t kernel, int32_t ks
  *   scales : M rows of ceil(K/32) bytes, row stride lds bytes.  Every row may
  *            be read up to its stride, so the buffer holds M * lds bytes.
  * Code strides and bases that are multiples of 16, and scale strides and
- * bases that are multiples of 16, take the matrix-core kernels; anything else
- * is read byte by byte (slow).
+ * bases that are multiples of 16 (8 suffices for M <= 64), take the matrix-core
+ * kernels; anything else is read byte by byte (slow).
  *
  * mgemm_quantize_mx4 -- X (M x K, row-major, element type xtype = F32, F16 or
  * BF16, ldx >= max(1, K)) to codes and scales.  Per block, amax = largest |x|
@@ -533,9 +533,9 @@ mgemm_status_t mgemm_run_mx4(mgemm_handle_t h, mgemm_kernel_t kernel, int32_t ks
 /*
  * mgemm_linear_mx4 -- Y = Q(X) B^T: X (M x K, row-major, type xtype, ldx) is
  * quantised as mgemm_quantize_mx4 does, within the call, and multiplied as
- * mgemm_run_mx4 does into Y (M x N, row-major, type ytype, ldy).  Up to 16 rows
+ * mgemm_run_mx4 does into Y (M x N, row-major, type ytype, ldy).  Few short rows
  * are quantised inside the product's own kernel (one launch, X rows 16-byte
- * aligned); more go through the handle's workspace, a band of rows at a time
+ * aligned); others go through the handle's workspace, a band of rows at a time
  * where they do not fit, so calls on different streams need different handles.
  * mgemm_gated_mx4 -- Z = SiLU(Q(X) Bg^T) (.) (Q(X) Bu^T) in the same way,
  * with both weight matrices N x K and shared strides: per output, with FP32
@@ -619,17 +619,15 @@ mgemm_status_t mgemm_gated_backward(mgemm_handle_t h, mgemm_layout_t layoutW, in
  * mgemm_run_variant does for a plain product (tests run every one).
  *   product : 0 the forward pair (also where it is computed again), 1 dX,
  *             2 the weights' gradients;
- *   rows, columns : 256 x 256 or 256 x 192; 128 x 128; 128 x 256 (product 0) or
- *             128 x 192 (products 1 and 2); product 0 counts the columns of
- *             both weights.  0, 0 (ksplit 0) returns to the library's choice.
- *   ksplit : ranges of the contraction as for mgemm_run_variant; 0 the
- *            library's choice.  A call whose forced ranges do not fit the
- *            handle's workspace returns MGEMM_ERR_UNSUPPORTED.
- * Errors: MGEMM_ERR_INVALID_ARG for a NULL handle or values out of range,
- * MGEMM_ERR_UNSUPPORTED for a tile that the product does not have.
+ *   size    : 256 or 128 rows and columns (product 0 counts the columns of both
+ *             weights), 0 the library's choice;
+ *   ksplit  : ranges of the contraction as for mgemm_run_variant, 0 the library's
+ *             choice.  A call whose forced ranges do not fit the handle's
+ *             workspace returns MGEMM_ERR_UNSUPPORTED.
+ * Errors: MGEMM_ERR_INVALID_ARG for a NULL handle or another value.
  */
-mgemm_status_t mgemm_set_gated_tile(mgemm_handle_t h, int32_t product, int32_t rows,
-                                    int32_t columns, int32_t ksplit);
+mgemm_status_t mgemm_set_gated_tile(mgemm_handle_t h, int32_t product, int32_t size,
+                                    int32_t ksplit);
 
 /*
  * mgemm_run_noalloc -- mgemm_run_variant without a handle and without any

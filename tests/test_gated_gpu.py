@@ -237,21 +237,57 @@ def test_backward_again(h, layout, M, N, K, dtype, pad):
     g, u = rounded(x @ wg, dtype), rounded(x @ wu, dtype)
     b = Block(h, layout, M, N, K, dtype, x, wg, wu, pad)
     zd = wide(dz, N + pad, dtype)
-    outs = b.backward(zd)
-    got = b.grads(outs)
-    for a, (y, lim) in zip(got, backward_bounds(x, wg, wu, g, u, dz, dtype)):
-        assert (np.abs(a - y) <= lim).all(), np.abs(a - y).max()
-    # The same G and U stored by the forward pass: the same bits.
+    limits = backward_bounds(x, wg, wu, g, u, dz, dtype)
+
+    def check(outs, which=(0, 1, 2)):
+        got = b.grads(outs)
+        for i in which:
+            y, lim = limits[i]
+            assert (np.abs(got[i] - y) <= lim).all(), (i, np.abs(got[i] - y).max())
+    check(b.backward(zd))
+    # The same G and U stored by the forward pass (another order of sums, perhaps), and each half alone.
     _, gd, ud = b.forward()
-    for a, c in zip(b.backward(zd, gd, ud), outs):
-        assert torch.equal(a, c)
-    # Inputs only, or weights only.
-    assert torch.equal(b.backward(zd, dw=False)[0], outs[0])
-    only = b.backward(zd, dx=False)
-    assert torch.equal(only[1], outs[1]) and torch.equal(only[2], outs[2])
+    check(b.backward(zd, gd, ud))
+    check(b.backward(zd, dw=False), (0,))
+    check(b.backward(zd, dx=False), (1, 2))
 
 
-# Sizes that take each tile (256x256, 256x192, 128x192), whole and split contractions, with tails.
+@pytest.mark.parametrize("size", [128, 256])
+@pytest.mark.parametrize("ksplit", [1, 2, 5, 32])
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("M,N,K", [(300, 424, 616), (130, 520, 1096)])
+def test_every_tile(h, size, ksplit, layout, M, N, K):
+    """Each product in each tile size and split, with tails of the contraction (sizes that are multiples of 8)."""
+    say("gated tile", size, ksplit, layout, M, N, K)
+    rng = np.random.default_rng(size + ksplit)
+    x, wg, wu, g, u, dz, dg, du = exact_case(rng, M, N, K)
+    want = [dg @ wg.T + du @ wu.T, x.T @ dg, x.T @ du]
+    for dtype in ("bf16", "f16"):
+        b = Block(h, layout, M, N, K, dtype, x, wg, wu)
+        args = [wide(v, N, dtype) for v in (dz, g, u)]
+        try:
+            for p in range(3):
+                mg.mgemm_set_gated_tile(h, p, size, ksplit)
+            z, gd, ud = b.forward()
+            outs = b.backward(*args)
+            plus = b.backward(*args, beta=2.0)
+            torch.cuda.synchronize()
+        finally:
+            for p in range(3):
+                mg.mgemm_set_gated_tile(h, p)
+        zo, go, uo = gated.forward(x, wg, wu)
+        assert np.array_equal(gd.double().cpu().numpy(), rounded(go, dtype))
+        assert np.array_equal(ud.double().cpu().numpy(), rounded(uo, dtype))
+        zs = z.double().cpu().numpy()
+        fits = np.abs(zo) < float(torch.finfo(TORCH[dtype]).max) * (1 - 2 * EPS[dtype])
+        assert (np.abs(zs - zo)[fits] <= ((EPS[dtype] + 4e-6) * np.abs(zo) + TINY[dtype])[fits]).all()
+        for a, w in zip(b.grads(outs), want):
+            assert np.array_equal(a, rounded(w, dtype))
+        for a, w in zip(b.grads(plus), [want[0], want[1] + 6.0, want[2] - 4.0]):
+            assert np.array_equal(a, rounded(w, dtype))
+
+
+# Sizes that take both tiles, whole and split contractions, with tails.
 @pytest.mark.parametrize("M,N,K", [(1024, 1536, 1100), (2100, 5000, 520), (515, 2048, 4100), (4100, 300, 1030),
                                    (3000, 3100, 1000)])
 @pytest.mark.parametrize("layout", ["row", "col"])

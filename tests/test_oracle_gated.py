@@ -115,3 +115,13 @@ def test_nothing_to_do():
     assert forward(N=0, z=None, g=None, u=None) == 0
     assert backward(dx=None, dwg=None, dwu=None) == 0
     assert backward(M=0, dx=None, dwg=None, dwu=None) == 0
+
+
+def test_tile_refusals():
+    set_tile = mg.load().mgemm_set_gated_tile
+    handle = ctypes.create_string_buffer(4096)
+    h = ctypes.addressof(handle)
+    assert set_tile(None, 0, 128, 1) == INVALID
+    for bad in ((-1, 128, 1), (3, 128, 1), (0, 64, 1), (0, 192, 0), (0, 128, -1), (0, 128, 33)):
+        assert set_tile(h, *bad) == INVALID
+    assert set_tile(h, 2, 256, 32) == 0 and set_tile(h, 2, 0, 0) == 0
