@@ -63,6 +63,7 @@ constexpr Shape SHAPES[] = {{MGEMM_KERNEL_MX4_MFMA, 256, 256},
 double tile_speed(const Problem& p, int bn, int bm) {
     if (bm == 64) return 0.37;
     if (bm == 128 && p.M <= 128) return 0.63;
+    if (bm == 256 && p.M <= 128) return 0.9;
     return bn == 256 ? 1.4 : 1.3;
 }
 

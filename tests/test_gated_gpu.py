@@ -401,3 +401,52 @@ def test_other_stream_and_graph(h):
             for a, c in zip(fouts + outs, list(want_f) + list(want_b)):
                 assert torch.equal(a, c), i
         del work, fkeep, bkeep
+
+
+def test_offsets_past_31_bits(h):
+    # 66000 x 33000 outputs: element and byte offsets beyond 2^31, in and out.
+    M, N, K = 66000, 33000, 64
+    gen = torch.Generator(device="cuda").manual_seed(2)
+
+    def pick(lo, hi, *shape):
+        return torch.randint(lo, hi + 1, shape, generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    say("gated large", M, N, K)
+    x, wg, wu = pick(-1, 1, M, K), pick(-1, 1, K, N), pick(-1, 1, K, N)
+    z, g, u = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    w = torch.empty(mg.mgemm_gated_workspace("row", M, N, K, x, K, wg, wu, N, "bf16", True, True), dtype=torch.uint8,
+                    device="cuda")
+    mg.mgemm_gated_forward(h, "row", M, N, K, x, K, wg, wu, N, z, N, g, u, N, "bf16", w, w.numel())
+    dx = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    dwg, dwu = torch.empty_like(wg), torch.empty_like(wu)
+    # Sums of up to 64 units are exact in BF16; the backward pass takes G = 0 or 32 (see exact_case).
+    for m in range(0, M, 6000):
+        go, uo = x[m:m + 6000].float() @ wg.float(), x[m:m + 6000].float() @ wu.float()
+        assert torch.equal(g[m:m + 6000].float(), go) and torch.equal(u[m:m + 6000].float(), uo)
+        zo = go.double() * torch.sigmoid(go.double()) * uo.double()
+        assert ((z[m:m + 6000].double() - zo).abs() <= (EPS["bf16"] + 4e-6) * zo.abs() + TINY["bf16"]).all()
+        del go, uo, zo
+    dz = z
+    for m in range(0, M, 6000):
+        g[m:m + 6000] = 32 * pick(0, 1, min(6000, M - m), N)
+        dz[m:m + 6000] = pick(-1, 1, min(6000, M - m), N)
+        u[m:m + 6000] = 2 * pick(-1, 1, min(6000, M - m), N)
+    mg.mgemm_gated_backward(h, "row", M, N, K, x, K, wg, wu, N, g, u, N, dz, N, dx, K, dwg, dwu, N, 0.0, "bf16", w,
+                            w.numel())
+    og, ou = torch.zeros(K, N, device="cuda", dtype=torch.float64), torch.zeros(K, N, device="cuda", dtype=torch.float64)
+    for m in range(0, M, 6000):
+        gs, us, ds, xs = (t[m:m + 6000].float() for t in (g, u, dz, x))
+        dg, du = torch.where(gs == 0, ds * us / 2, ds * us), torch.where(gs == 0, 0.0, 32 * ds)
+        # Products of integers, sums below 2^24: exact in 32 bits.
+        assert torch.equal(dx[m:m + 6000], (dg @ wg.float().t() + du @ wu.float().t()).bfloat16())
+        og += (xs.t() @ dg).double()
+        ou += (xs.t() @ du).double()
+        del gs, us, ds, dg, du
+    assert torch.equal(dwg, og.bfloat16()) and torch.equal(dwu, ou.bfloat16())
+
+
+def test_example_trains_and_serves():
+    import examples.gated_block as example
+    losses, off = example.main(steps=30)
+    assert losses[-1] < 0.6 * losses[0]
+    # E2M1 keeps about 3 bits of each operand: 10 to 20% of the norm for products of normal values.
+    assert 0.01 < off < 0.35
