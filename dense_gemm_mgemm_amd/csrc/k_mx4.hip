@@ -429,7 +429,15 @@ __global__ __launch_bounds__(NT) void k_mx4_reduce(Problem p, Mx4Args f) {
     auto sum = [&](int chunk) {
         const float* src = tile + (int64_t)chunk * NT * 4;
         f32x4 a = *(const f32x4*)src;
-        for (int s = 1; s < f.ksplit; ++s) a = a + *(const f32x4*)(src + s * TILE);
+        // Eight ranges are requested at a time and added one by one.
+        for (int s = 1; s < f.ksplit; s += 8) {
+            f32x4 b[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = s + i < f.ksplit ? *(const f32x4*)(src + (s + i) * TILE) : f32x4{};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (s + i < f.ksplit) a = a + b[i];
+        }
         return a;
     };
     const f32x4 g = sum((tm * TN + tn) * 4 + q);

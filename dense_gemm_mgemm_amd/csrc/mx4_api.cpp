@@ -56,15 +56,16 @@ constexpr Shape SHAPES[] = {{MGEMM_KERNEL_MX4_MFMA, 256, 256},
                             {MGEMM_KERNEL_MX4_MFMA_128, 192, 128},
                             {MGEMM_KERNEL_MX4_MFMA_64, 192, 64}};
 
-// A tile's rate in the time model.  Few rows stream the weights from HBM: a
-// slice of the 64-row tile then takes 0.5 us whatever it computes and of the
-// 128-row tile 0.58 (48 x 4096 x 12288 in 8 ranges 14.6 and 16.8 us; 48 x 12288
-// x 4096 whole 18.4, in 4 ranges 12.9), more than their matrix time.
+// A tile's rate in the time model, from what a 128-element slice of it takes:
+// 64x192 0.5 us, 128x192 0.75 (0.58 for few rows, which stream the weights from
+// HBM whatever they compute), 256x192 1.0, 256x256 1.22 (300 x 5000 x 2000 on
+// 64 / 128 rows 12.4 / 16.8 us; 1000^3 8.8 / 11.7; 8192 x 12288 x 4096 on 64 / 128 /
+// 256 x 192 and 256 x 256 480 / 416 / 329 / 294; 48 x 12288 x 4096 whole 18.4, in
+// 4 ranges 12.3).
 double tile_speed(const Problem& p, int bn, int bm) {
     if (bm == 64) return 0.37;
-    if (bm == 128 && p.M <= 128) return 0.63;
-    if (bm == 256 && p.M <= 128) return 0.9;
-    return bn == 256 ? 1.4 : 1.3;
+    if (bm == 128) return p.M <= 128 ? 0.63 : 0.49;
+    return bn == 256 ? 0.80 : 0.735;
 }
 
 // The split with the smallest predicted time for one tile shape.  A
@@ -81,7 +82,8 @@ Tile best_split(const Problem& p, int bn, int bm, const Workspace& ws, double* t
         const int ks = mgemm::mx4_splits(p, bn, bm, req, ws);
         if (ks <= last) continue;
         last = ks;
-        const double t = predict_us(q, bm, bn, out, tile_speed(p, bn, bm), 1, ks, 4.5e6);
+        // (A range also costs the thread that adds it 0.3 us.)
+        const double t = predict_us(q, bm, bn, out, tile_speed(p, bn, bm), 1, ks, 4.5e6) + (ks > 1 ? 0.3 * ks : 0.0);
         if (t < bt) { bt = t; best.ks = ks; }
     }
     *t_out = bt;
@@ -91,9 +93,9 @@ Tile best_split(const Problem& p, int bn, int bm, const Workspace& ws, double* t
 // Predicted time (microseconds) of the decode kernel on codes: a launch, then
 // per 4096 columns (a 16-column workgroup on each CU; the gated pair has both
 // matrices') and 1024 elements of K (a slice for each wave) 0.023 us a row.
-// Measured on 4096 x 12288 weights: M = 17 / 32 / 48 / 64 12.0 / 14.3 / 20.4 /
-// 22.8 us, against 13.3 / 13.7 / 14.6 / 15.4 on 64-row tiles in 8 ranges; 12288
-// x 4096: M = 1 / 16 9.0 / 10.4 against 9.8 / 10.2 in 4; 40 x 1000 x 1000 6.0
+// Measured on 4096 x 12288 weights: M = 17 / 32 / 48 / 64 12.0 / 14.2 / 20.5 /
+// 22.7 us, against 12.0 / 12.5 / 13.4 / 14.3 on 64-row tiles in 8 ranges; 12288
+// x 4096: M = 1 / 16 8.6 / 10.4 against 9.8 / 10.4 in 4; 40 x 1000 x 1000 6.0
 // against 8.0.
 double skinny_us(const Problem& p) {
     const int64_t n = p.B2 != nullptr ? 2 * p.N : p.N;
