@@ -298,3 +298,15 @@ def test_other_stream_and_graph(h):
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, z), (M, i)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 50, 700), (20, 70, 1500), (64, 33, 250)])
+def test_scale_rows_of_eight_bytes(h, M, N, K):
+    # Scale strides that are multiples of 8 and not of 16: the decode kernel, whose last load ends with the row.
+    rng = np.random.default_rng(K)
+    nb = -(-K // 32)
+    lds = up(nb, 8) + (8 if up(nb, 8) % 16 == 0 else 0)
+    a, b = codes(rng, M, K, 16 * nb, lds), codes(rng, N, K, 16 * nb, lds)
+    for kernel in ("auto", "mx4_skinny"):
+        say("run_mx4 scale stride", lds, kernel, M, N, K)
+        assert np.array_equal(product(h, kernel, M, N, K, a, b).cpu().double().numpy(), a[2] @ b[2].T)
