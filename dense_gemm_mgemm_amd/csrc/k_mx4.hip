@@ -454,7 +454,10 @@ __global__ __launch_bounds__(NT) void k_mx4_reduce(Problem p, Mx4Args f) {
 }
 
 // Any alignment and stride: 64x64 output tiles, one block of 32 per step
-// decoded to FP32 in LDS, a 4x4 register block per thread, fmaf in K order.
+// decoded to FP32 in LDS, a 4x4 register block per thread.  A block's products
+// are multiples of 1/4 up to 36, so its sum is exact; both scales are applied to
+// the sum in one step, because a value times its own scale alone leaves FP32's
+// range from scale byte 253 on while the product may lie well inside it.
 constexpr int GT = 64;
 
 template <int CT, bool DUAL>
@@ -462,6 +465,7 @@ __global__ __launch_bounds__(NT) void k_mx4_general(Problem p, Mx4Args f) {
     constexpr int NB = DUAL ? 2 : 1;
     __shared__ float As[MX_BLOCK][GT + 4];
     __shared__ float Bs[NB][MX_BLOCK][GT + 4];
+    __shared__ int Ea[GT], Eb[NB][GT];                     // scale bytes of the block
     const int tid = threadIdx.x;
     const int tiles_n = (int)((p.N + GT - 1) / GT);
     const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * GT, n0 = (int64_t)(blockIdx.x % tiles_n) * GT;
@@ -469,7 +473,7 @@ __global__ __launch_bounds__(NT) void k_mx4_general(Problem p, Mx4Args f) {
     const int tx = tid & 15, ty = tid >> 4;
     float acc[NB][4][4] = {};
     auto stage = [&](const void* codes, int64_t ld, const uint8_t* scales, int64_t lds, int64_t row, int64_t rows,
-                     int64_t b, float (*to)[GT + 4]) {
+                     int64_t b, float (*to)[GT + 4], int* exps) {
         uint32_t w = 0, sc = 127;
         if (row < rows) {
             const uint8_t* q = (const uint8_t*)codes + row * ld + b * 16 + part * 4;
@@ -478,14 +482,16 @@ __global__ __launch_bounds__(NT) void k_mx4_general(Problem p, Mx4Args f) {
             sc = scales[row * lds + b];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) to[part * 8 + e][r] = mx4_scaled(mx4_value(w >> (4 * e)), sc);
+        for (int e = 0; e < 8; ++e) to[part * 8 + e][r] = mx4_value(w >> (4 * e));
+        if (part == 0) exps[r] = (int)sc;
     };
     const int64_t blocks = (p.K + MX_BLOCK - 1) / MX_BLOCK;
     for (int64_t b = 0; b < blocks; ++b) {
-        stage(p.A, p.lda, f.sa, f.ldsa, m0 + r, p.M, b, As);
-        stage(p.B, p.ldb, f.sb, f.ldsb, n0 + r, p.N, b, Bs[0]);
-        if constexpr (DUAL) stage(p.B2, p.ldb, f.sb2, f.ldsb, n0 + r, p.N, b, Bs[1]);
+        stage(p.A, p.lda, f.sa, f.ldsa, m0 + r, p.M, b, As, Ea);
+        stage(p.B, p.ldb, f.sb, f.ldsb, n0 + r, p.N, b, Bs[0], Eb[0]);
+        if constexpr (DUAL) stage(p.B2, p.ldb, f.sb2, f.ldsb, n0 + r, p.N, b, Bs[1], Eb[1]);
         __syncthreads();
+        float sum[NB][4][4] = {};
 #pragma unroll 4
         for (int k = 0; k < MX_BLOCK; ++k)
 #pragma unroll
@@ -494,7 +500,17 @@ __global__ __launch_bounds__(NT) void k_mx4_general(Problem p, Mx4Args f) {
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[h][i][j] = fmaf(As[k][ty * 4 + i], Bs[h][k][tx * 4 + j], acc[h][i][j]);
+                        sum[h][i][j] = fmaf(As[k][ty * 4 + i], Bs[h][k][tx * 4 + j], sum[h][i][j]);
+#pragma unroll
+        for (int h = 0; h < NB; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int ea = Ea[ty * 4 + i], eb = Eb[h][tx * 4 + j];
+                    const float v = __builtin_amdgcn_ldexpf(sum[h][i][j], ea + eb - 254);
+                    acc[h][i][j] += ea == 255 || eb == 255 ? __uint_as_float(0x7FC00000u) : v;
+                }
         __syncthreads();
     }
 #pragma unroll

@@ -518,8 +518,10 @@ mgemm_status_t mgemm_dequantize_mx4(mgemm_handle_t h, int64_t M, int64_t K, cons
  *   kernel, ksplit : as for mgemm_run_fp8, with MGEMM_KERNEL_AUTO or one of
  *           the MGEMM_KERNEL_MX4_* kernels; K is split into ranges of whole
  *           128-element slices (MFMA tiles only), the ranges summed in order.
- * Products of codes and scales are exact; sums are FP32.  A block whose scale
- * is 255 makes every output of its row or column NaN.
+ * Products of codes and scales are exact; sums are FP32.  The two scales of a
+ * product are applied together: bytes 253 and 254, whose larger values are past
+ * FP32's range, give finite products where the other scale brings them back.  A
+ * block whose scale is 255 makes every output of its row or column NaN.
  * M == 0 or N == 0 does nothing; K == 0 or alpha == 0 gives C = beta * C.
  * Asynchronous on `stream`.  The split form uses the handle's workspace.
  * Errors: as mgemm_run_fp8.
