@@ -214,6 +214,32 @@ __device__ __forceinline__ float silu_f32(float c) {
         return tail ? (c * e) * 0x1p-64f : head;
     }
 }
+// Sigmoid of a gate as m * 2^e, from the hardware exp2 and reciprocal (relative
+// error near 1e-6).  Below -20, where 1 + e^-g is e^-g to 2^-28, it is e^g with
+// the power of two split off: a sigmoid that is subnormal or zero in FP32 keeps
+// its bits until it meets the factors that bring the product back into range.
+// There m is in [2^-11, 2^-10): down to g = -1000 (e^g is 2^-1443) g * m and
+// (1 + g) * m stay below 1, and a product with them overflows only where its
+// other factors do.
+constexpr float GATE_TAIL = -20.0f;
+struct Gate {
+    float m;
+    int e;
+    bool tail;      // e^g form: 1 - m * 2^e is 1 in FP32
+};
+__device__ __forceinline__ Gate gate_of(float g) {
+    constexpr float LOG2E = 1.44269504088896341f, LOG2E_LO = 1.92596299e-8f;   // their sum is log2(e) to 48 bits
+    const bool tail = !(g >= GATE_TAIL);              // also NaN in, NaN out
+    const float t = g * LOG2E;
+    // Below 2^-1400 every product is zero; the bound keeps the exponent an int.
+    const float n = floorf(fmaxf(t, -1500.0f)) + 11.0f;
+    const float p = __builtin_amdgcn_exp2f(tail ? fmaf(g, LOG2E_LO, fmaf(g, LOG2E, -n)) : -t);
+    return Gate{tail ? p : __builtin_amdgcn_rcpf(1.0f + p), tail ? (int)n : 0, tail};
+}
+// The same bits for g >= GATE_TAIL (and NaN), where e is 0.
+__device__ __forceinline__ float near_sigmoid(float g) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-(g * 1.44269504088896341f)));
+}
 template <int DT, int EPI>
 __device__ __forceinline__ float epilogue_op(float v) {
     if constexpr (EPI == EPI_SILU) return silu_f32<DT>(round_trip<DT>(v));

@@ -150,24 +150,54 @@ struct Frags {
     i32x4 b[TN];
 };
 
-// s = 1 / (1 + e^-g) from the hardware exp2 and reciprocal (relative errors
-// near 1e-6, far below the 16-bit roundings that follow); e^g where 1 + e^-g
-// would round to e^-g, so that e^-g does not overflow.
-__device__ __forceinline__ float sigmoid_f32(float g) {
-    constexpr float LOG2E = 1.44269504088896341f;
-    const bool tail = !(g >= -20.0f);            // also NaN in, NaN out
-    const float e = __builtin_amdgcn_exp2f(tail ? g * LOG2E : -g * LOG2E);
-    return tail ? e : __builtin_amdgcn_rcpf(1.0f + e);
-}
-__device__ __forceinline__ void gated_grad(float g, float u, float dz, float& dg, float& du) {
-    const float s = sigmoid_f32(g);
-    du = dz * (g * s);
-    dg = dz * u * (s * fmaf(g, 1.0f - s, 1.0f));
+// dG and dU of N outputs.  The sigmoid's power of two comes last (Gate): with a
+// gate at -88 s is 6e-39, which FP32 arithmetic without subnormal exp2 results
+// takes for 0, and dZ U s (1 + G) may still be any number.  Gates below -20 are
+// rare, and their form costs nine more operations an output (dG and dU of 1024 x
+// 12288: 4 us), so only waves that hold one take it; the other gives the same
+// bits at -20 and above.
+template <int N>
+__device__ __forceinline__ void gated_grad(const float (&g)[N], const float (&u)[N], const float (&dz)[N],
+                                           float (&dg)[N], float (&du)[N]) {
+    bool far = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) far |= !(g[i] >= GATE_TAIL);
+    if (far) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const Gate s = gate_of(g[i]);
+            const float rest = s.tail ? 1.0f : 1.0f - s.m;               // 1 - s
+            du[i] = __builtin_amdgcn_ldexpf(dz[i] * (g[i] * s.m), s.e);
+            dg[i] = __builtin_amdgcn_ldexpf(dz[i] * u[i] * (s.m * fmaf(g[i], rest, 1.0f)), s.e);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float s = near_sigmoid(g[i]);
+            du[i] = dz[i] * (g[i] * s);
+            dg[i] = dz[i] * u[i] * (s * fmaf(g[i], 1.0f - s, 1.0f));
+        }
+    }
     // Both products are rounded to FP32 here.  Left to itself the compiler
     // folds some of them into the conversion to FP16 that follows (one
     // rounding in place of two), in one caller and not in another, and
     // recomputed G and U would not give the bits of stored ones.
-    asm("" : "+v"(dg), "+v"(du));
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm("" : "+v"(dg[i]), "+v"(du[i]));
+}
+
+// Sums g and u, rounded as the forward pass stores them, to dG and dU.
+template <int DT>
+__device__ __forceinline__ void gated_grad_of(f32x4& g, f32x4& u, const float (&dz)[4]) {
+    float gs[4], us[4], a[4], b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        gs[e] = round_trip<DT>(g[e]);
+        us[e] = round_trip<DT>(u[e]);
+    }
+    gated_grad(gs, us, dz, a, b);
+    g = f32x4{a[0], a[1], a[2], a[3]};
+    u = f32x4{b[0], b[1], b[2], b[3]};
 }
 
 // Four consecutive 16-bit elements of a row (zero past lim).
@@ -556,13 +586,7 @@ __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblo
                         if (m < f.Mz)
                             load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n0, wcol0 + c,
                                       (int)(f.Nz - n0 < G::OUT ? f.Nz - n0 : G::OUT), vec4_ok(f.dZ, f.ldz), dz);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float a, b;
-                            gated_grad(round_trip<DT>(g[e]), round_trip<DT>(u[e]), dz[e], a, b);
-                            g[e] = a;
-                            u[e] = b;
-                        }
+                        gated_grad_of<DT>(g, u, dz);
                     }
 #pragma unroll
                     for (int pl = 0; pl < NP; ++pl) {
@@ -663,13 +687,7 @@ __device__ __forceinline__ void reduce_body(const BlockArgs& f, int bid, int nbl
         if (m < f.Mz)
             load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n0, ni, (int)(f.Nz - n0 < G::OUT ? f.Nz - n0 : G::OUT),
                       vec4_ok(f.dZ, f.ldz), dz);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float a, b;
-            gated_grad(round_trip<DT>(g[e]), round_trip<DT>(u[e]), dz[e], a, b);
-            g[e] = a;
-            u[e] = b;
-        }
+        gated_grad_of<DT>(g, u, dz);
     }
 #pragma unroll
     for (int plane = 0; plane < planes<FORM>(); ++plane) {

@@ -42,8 +42,7 @@ __global__ __launch_bounds__(NT) void k_gated_grad(uint32_t total, uint32_t per_
     load8<DT>(G + row * ldg + n, left, vec, g);
     load8<DT>(U + row * ldg + n, left, vec, u);
     load8<DT>(dZ + row * lddz + n, left, vec, dz);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) gated_grad(g[e], u[e], dz[e], a[e], b[e]);
+    gated_grad(g, u, dz, a, b);
     store8<DT>(dG + row * ldd + n, a);
     store8<DT>(dU + row * ldd + n, b);
 }

@@ -38,3 +38,18 @@ def test_gradients_of_closed_gates(h, again):  # noqa: F811
         assert np.isfinite(got).all()
         off = np.abs(got - ref) > (EPS["bf16"] + 1e-5) * np.abs(ref) + TINY["bf16"]
         assert not off.any(), [(FAR[i], got[i, j], ref[i, j]) for i, j in np.argwhere(off)[:4]]
+
+
+def test_one_closed_gate_leaves_the_others_bits(h):  # noqa: F811
+    """A wave that holds a closed gate takes another form of the sigmoid: its other outputs keep their bits."""
+    n = 64
+    rng = np.random.default_rng(6)
+    g, u, dz = (rounded(v, "bf16") for v in (rng.uniform(-19.9, 19.9, (n, n)), rng.standard_normal((n, n)),
+                                             rng.standard_normal((n, n))))
+    b = Block(h, "row", n, n, n, "bf16", np.eye(n), np.zeros((n, n)), np.zeros((n, n)))
+    _, dwg, dwu = b.grads(b.backward(*(wide(v, n, "bf16") for v in (dz, g, u))))
+    g[::7, 5] = -95.0
+    _, awg, awu = b.grads(b.backward(*(wide(v, n, "bf16") for v in (dz, g, u))))
+    keep = np.ones((n, n), bool)
+    keep[::7, 5] = False
+    assert np.array_equal(dwg[keep], awg[keep]) and np.array_equal(dwu[keep], awu[keep])
