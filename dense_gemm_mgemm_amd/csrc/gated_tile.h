@@ -219,11 +219,12 @@ __device__ __forceinline__ bool vec4_ok(const void* p, int64_t ld) { return ld %
 // Four outputs of plane `plane` (forward: Z, G, U; recomputed backward: dG, dU)
 // before their one rounding.  g: the sums of dX, dW or G, or dG; u: of U, or dU.
 // Z comes from the unrounded sums.
-template <int DT, int FORM>
+template <int DT, int FORM, bool FAR>
 __device__ __forceinline__ void block_value(int plane, f32x4 g, f32x4 u, float (&v)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if constexpr (FORM == BLOCK_FORWARD) v[e] = plane == 0 ? silu_f32<DT>(g[e]) * u[e] : plane == 1 ? g[e] : u[e];
+        if constexpr (FORM == BLOCK_FORWARD)
+            v[e] = plane == 0 ? gated_product<DT, FAR>(g[e], u[e]) : plane == 1 ? g[e] : u[e];
         else v[e] = plane == 0 ? g[e] : u[e];
     }
 }
@@ -569,34 +570,44 @@ __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblo
             const int r0 = 32 * tm, fr = lane & 31, nq = 4 * (lane >> 5);
             const int rows = mlim - wrow0 - r0 < 32 ? mlim - wrow0 - r0 : 32;
             wave_fence();
+            auto stage = [&](auto far) {
 #pragma unroll
-            for (int tn = 0; tn < G::TNO; ++tn)
+                for (int tn = 0; tn < G::TNO; ++tn)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    f32x4 g, u = f32x4{};
+                    for (int q = 0; q < 4; ++q) {
+                        f32x4 g, u = f32x4{};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        g[e] = from_acc(acc[tm][tn][4 * q + e]);
-                        if constexpr (DUAL) u[e] = from_acc(acc[tm][tn + TN - G::TNO][4 * q + e]);
+                        for (int e = 0; e < 4; ++e) {
+                            g[e] = from_acc(acc[tm][tn][4 * q + e]);
+                            if constexpr (DUAL) u[e] = from_acc(acc[tm][tn + TN - G::TNO][4 * q + e]);
+                        }
+                        const int c = 32 * tn + 8 * q + nq;
+                        if constexpr (FORM == BLOCK_AGAIN) {
+                            float dz[4] = {};
+                            const int64_t m = m0 + wrow0 + r0 + fr;
+                            if (m < f.Mz)
+                                load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n0, wcol0 + c,
+                                          (int)(f.Nz - n0 < G::OUT ? f.Nz - n0 : G::OUT), vec4_ok(f.dZ, f.ldz), dz);
+                            gated_grad_of<DT>(g, u, dz);
+                        }
+#pragma unroll
+                        for (int pl = 0; pl < NP; ++pl) {
+                            float v[4];
+                            block_value<DT, FORM, decltype(far)::value>(pl, g, u, v);
+                            *(uint2*)(st + pl * PIECE + fr * G::STAGE_ROW + c * 2) =
+                                make_uint2((uint32_t)to_bits<DT>(v[0]) | ((uint32_t)to_bits<DT>(v[1]) << 16),
+                                           (uint32_t)to_bits<DT>(v[2]) | ((uint32_t)to_bits<DT>(v[3]) << 16));
+                        }
                     }
-                    const int c = 32 * tn + 8 * q + nq;
-                    if constexpr (FORM == BLOCK_AGAIN) {
-                        float dz[4] = {};
-                        const int64_t m = m0 + wrow0 + r0 + fr;
-                        if (m < f.Mz)
-                            load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n0, wcol0 + c,
-                                      (int)(f.Nz - n0 < G::OUT ? f.Nz - n0 : G::OUT), vec4_ok(f.dZ, f.ldz), dz);
-                        gated_grad_of<DT>(g, u, dz);
-                    }
+            };
+            if constexpr (FORM == BLOCK_FORWARD) {
+                uint32_t bits = 0;
 #pragma unroll
-                    for (int pl = 0; pl < NP; ++pl) {
-                        float v[4];
-                        block_value<DT, FORM>(pl, g, u, v);
-                        *(uint2*)(st + pl * PIECE + fr * G::STAGE_ROW + c * 2) =
-                            make_uint2((uint32_t)to_bits<DT>(v[0]) | ((uint32_t)to_bits<DT>(v[1]) << 16),
-                                       (uint32_t)to_bits<DT>(v[2]) | ((uint32_t)to_bits<DT>(v[3]) << 16));
-                    }
-                }
+                for (int i = 0; i < G::TNO * 16; ++i) bits = max_bits(bits, from_acc(acc[tm][i / 16][i % 16]));
+                with_far(any_far(bits), stage);
+            } else {
+                stage(std::false_type{});
+            }
             wave_fence();
 #pragma unroll
             for (int pl = 0; pl < NP; ++pl) {
@@ -695,7 +706,9 @@ __device__ __forceinline__ void reduce_body(const BlockArgs& f, int bid, int nbl
         uint16_t* C = plane_of<FORM>(f, plane, bt, ld);
         if (FORM == BLOCK_FORWARD && C == nullptr) continue;
         float v[4];
-        block_value<DT, FORM>(plane, g, u, v);
+        if (FORM == BLOCK_FORWARD && plane == 0)
+            gated_product4<DT>({g[0], g[1], g[2], g[3]}, {u[0], u[1], u[2], u[3]}, v);
+        else block_value<DT, FORM, false>(plane, g, u, v);
         store_out4<DT, EPI_NONE>(C + m * ld + n0, ni, nlim, vec4_ok(C, ld), f.beta, v);
     }
 }

@@ -106,12 +106,6 @@ struct Scales {
     int b[TN];
 };
 
-// Gated output from the FP32 sums, rounded once by the store.
-template <int CT>
-__device__ __forceinline__ float gated_out(float g, float u) {
-    return silu_f32<CT>(g) * u;
-}
-
 template <int CT, int BN, int BM, bool DUAL, bool PARTIAL>
 __global__ __launch_bounds__(NT, 1) void k_mx4_dma(Problem p, Mx4Args f) {
     using G = Cfg<BN, BM, DUAL>;
@@ -387,18 +381,29 @@ __global__ __launch_bounds__(NT, 1) void k_mx4_dma(Problem p, Mx4Args f) {
         const int mi = G::WROWS * wm + 32 * tm + fr;
         if (mi >= mlim) continue;
         const int64_t row = (m0 + mi) * p.ldc + n0;
+        auto store = [&](auto far) {
 #pragma unroll
-        for (int tn = 0; tn < (DUAL ? TN / 2 : TN); ++tn)
+            for (int tn = 0; tn < (DUAL ? TN / 2 : TN); ++tn)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[4];
+                for (int q = 0; q < 4; ++q) {
+                    float v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (DUAL) v[e] = gated_out<CT>(acc[tm][tn][4 * q + e], acc[tm][tn + TN / 2][4 * q + e]);
-                    else v[e] = p.alpha * acc[tm][tn][4 * q + e];
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (DUAL)
+                            v[e] = gated_product<CT, far>(acc[tm][tn][4 * q + e], acc[tm][tn + TN / 2][4 * q + e]);
+                        else v[e] = p.alpha * acc[tm][tn][4 * q + e];
+                    }
+                    mx4_store4<CT>(p.C, row, G::WN * wn + 32 * tn + 8 * q + nq, nlim, vec_ok, p.beta, v);
                 }
-                mx4_store4<CT>(p.C, row, G::WN * wn + 32 * tn + 8 * q + nq, nlim, vec_ok, p.beta, v);
-            }
+        };
+        if constexpr (DUAL) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int i = 0; i < TN / 2 * 16; ++i) bits = max_bits(bits, acc[tm][i / 16][i % 16]);
+            with_far(any_far(bits), store);
+        } else {
+            store(std::false_type{});
+        }
     }
     clock_stamp_end(p, stamp0);
 }
@@ -444,8 +449,7 @@ __global__ __launch_bounds__(NT) void k_mx4_reduce(Problem p, Mx4Args f) {
     float v[4];
     if constexpr (DUAL) {
         const f32x4 u = sum((tm * TN + tn + TN / 2) * 4 + q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = gated_out<CT>(g[e], u[e]);
+        gated_product4<CT>({g[0], g[1], g[2], g[3]}, {u[0], u[1], u[2], u[3]}, v);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = p.alpha * g[e];
@@ -518,10 +522,11 @@ __global__ __launch_bounds__(NT) void k_mx4_general(Problem p, Mx4Args f) {
         const int64_t m = m0 + ty * 4 + i;
         if (m >= p.M) continue;
         float v[4];
+        if constexpr (DUAL) {
+            gated_product4<CT>(acc[0][i], acc[1][i], v);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (DUAL) v[j] = gated_out<CT>(acc[0][i][j], acc[1][i][j]);
-            else v[j] = p.alpha * acc[0][i][j];
+            for (int j = 0; j < 4; ++j) v[j] = p.alpha * acc[0][i][j];
         }
         const int nlim = (int)(p.N - n0 < GT ? p.N - n0 : GT);
         mx4_store4<CT>(p.C, m * p.ldc + n0, tx * 4, nlim, mx4_vec_ok<CT>(p.C, p.ldc), p.beta, v);

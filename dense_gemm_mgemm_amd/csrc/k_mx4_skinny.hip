@@ -232,8 +232,7 @@ __global__ __launch_bounds__(NT) void k_mx4_skinny(Problem p, Mx4Args f) {
     float v[4];
     if constexpr (NB == 2) {
         const f32x4 u = sum((t * NB + 1) * MT + mt);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = silu_f32<CT>(g[e]) * u[e];
+        gated_product4<CT>({g[0], g[1], g[2], g[3]}, {u[0], u[1], u[2], u[3]}, v);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = p.alpha * g[e];
