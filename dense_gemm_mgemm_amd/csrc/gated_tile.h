@@ -186,20 +186,6 @@ __device__ __forceinline__ void gated_grad(const float (&g)[N], const float (&u)
     for (int i = 0; i < N; ++i) asm("" : "+v"(dg[i]), "+v"(du[i]));
 }
 
-// Sums g and u, rounded as the forward pass stores them, to dG and dU.
-template <int DT>
-__device__ __forceinline__ void gated_grad_of(f32x4& g, f32x4& u, const float (&dz)[4]) {
-    float gs[4], us[4], a[4], b[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        gs[e] = round_trip<DT>(g[e]);
-        us[e] = round_trip<DT>(u[e]);
-    }
-    gated_grad(gs, us, dz, a, b);
-    g = f32x4{a[0], a[1], a[2], a[3]};
-    u = f32x4{b[0], b[1], b[2], b[3]};
-}
-
 // Four consecutive 16-bit elements of a row (zero past lim).
 template <int DT>
 __device__ __forceinline__ void load4(const uint16_t* row, int n, int lim, bool vec_ok, float (&v)[4]) {
@@ -215,6 +201,25 @@ __device__ __forceinline__ void load4(const uint16_t* row, int n, int lim, bool 
     }
 }
 __device__ __forceinline__ bool vec4_ok(const void* p, int64_t ld) { return ld % 4 == 0 && ((uintptr_t)p & 7) == 0; }
+
+// Sums g and u of outputs (m, n .. n+3), rounded as the forward pass stores them,
+// to dG and dU.  Past dZ, in the rows and columns that a copied operand is padded
+// with, the results are zeros whatever the sums: 0 times an infinite weight is
+// not.
+template <int DT>
+__device__ __forceinline__ void again_grad(const BlockArgs& f, int64_t m, int64_t n, f32x4& g, f32x4& u) {
+    const int lim = m < f.Mz ? (int)(f.Nz - n < 4 ? f.Nz - n : 4) : 0;          // outputs that exist (none if <= 0)
+    float gs[4], us[4], dz[4], a[4], b[4];
+    load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n, 0, lim, vec4_ok(f.dZ, f.ldz), dz);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        gs[e] = e < lim ? round_trip<DT>(g[e]) : 0.0f;
+        us[e] = e < lim ? round_trip<DT>(u[e]) : 0.0f;
+    }
+    gated_grad(gs, us, dz, a, b);
+    g = f32x4{a[0], a[1], a[2], a[3]};
+    u = f32x4{b[0], b[1], b[2], b[3]};
+}
 
 // Four outputs of plane `plane` (forward: Z, G, U; recomputed backward: dG, dU)
 // before their one rounding.  g: the sums of dX, dW or G, or dG; u: of U, or dU.
@@ -583,12 +588,7 @@ __device__ __forceinline__ void block_body(const BlockArgs& f, int bid, int nblo
                         }
                         const int c = 32 * tn + 8 * q + nq;
                         if constexpr (FORM == BLOCK_AGAIN) {
-                            float dz[4] = {};
-                            const int64_t m = m0 + wrow0 + r0 + fr;
-                            if (m < f.Mz)
-                                load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n0, wcol0 + c,
-                                          (int)(f.Nz - n0 < G::OUT ? f.Nz - n0 : G::OUT), vec4_ok(f.dZ, f.ldz), dz);
-                            gated_grad_of<DT>(g, u, dz);
+                            again_grad<DT>(f, m0 + wrow0 + r0 + fr, n0 + wcol0 + c, g, u);
                         }
 #pragma unroll
                         for (int pl = 0; pl < NP; ++pl) {
@@ -694,11 +694,7 @@ __device__ __forceinline__ void reduce_body(const BlockArgs& f, int bid, int nbl
     f32x4 g = sum((tm * TN + tn) * 4 + q);
     f32x4 u = G::DUAL ? sum((tm * TN + tn + TNO) * 4 + q) : g;
     if constexpr (FORM == BLOCK_AGAIN) {
-        float dz[4] = {};
-        if (m < f.Mz)
-            load4<DT>((const uint16_t*)f.dZ + m * f.ldz + n0, ni, (int)(f.Nz - n0 < G::OUT ? f.Nz - n0 : G::OUT),
-                      vec4_ok(f.dZ, f.ldz), dz);
-        gated_grad_of<DT>(g, u, dz);
+        again_grad<DT>(f, m, n0 + ni, g, u);
     }
 #pragma unroll
     for (int plane = 0; plane < planes<FORM>(); ++plane) {
