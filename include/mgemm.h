@@ -590,7 +590,10 @@ mgemm_status_t mgemm_gated_mx4(mgemm_handle_t h, int64_t M, int64_t N, int64_t K
  * G and U are the forward pass's stored matrices, or both NULL: they are
  * computed again, rounded as the forward pass would have stored them.  dG and
  * dU are rounded to dtype between the two stages, as the operands of the
- * products have to be.  M == 0 or N == 0: dX = 0 and dW = beta * dW.
+ * products have to be: in FP16 one above 65504 is infinite and one below 2^-25
+ * zero, whatever the gradients would be, so dZ is scaled there as FP16 training
+ * scales its loss; BF16 has FP32's range.  M == 0 or N == 0: dX = 0 and
+ * dW = beta * dW.
  *
  * Errors: MGEMM_ERR_INVALID_ARG for negative sizes, an unknown layout or type,
  * a leading dimension that is too small, one of a pair NULL without the other,
