@@ -43,7 +43,7 @@ EXPORTED = ["mgemm_create", "mgemm_destroy", "mgemm_run", "mgemm_run_kernel", "m
             "mgemm_kernel_name", "mgemm_num_cu", "mgemm_run_noalloc", "mgemm_set_clock_stamps",
             "mgemm_run_acc32", "mgemm_quantize_mx4", "mgemm_dequantize_mx4", "mgemm_run_mx4",
             "mgemm_linear_mx4", "mgemm_gated_mx4", "mgemm_gated_workspace",
-            "mgemm_gated_forward", "mgemm_gated_backward", "mgemm_set_gated_tile"]
+            "mgemm_gated_forward", "mgemm_gated_backward", "mgemm_set_gated_tile", "mgemm_set_mx4_kernel"]
 
 
 class MgemmError(RuntimeError):
@@ -118,8 +118,9 @@ def load(path: str | None = None):
     lib.mgemm_linear_mx4.argtypes = [vp, i64, i64, i64, vp, i64, ci, vp, i64, vp, i64, vp, i64, ci, vp]
     lib.mgemm_gated_mx4.argtypes = [vp, i64, i64, i64, vp, i64, ci, vp, vp, vp, vp, i64, i64, vp, i64,
                                     ci, vp]
+    lib.mgemm_set_mx4_kernel.argtypes = [vp, ci, ctypes.c_int32]
     for name in ("mgemm_quantize_mx4", "mgemm_dequantize_mx4", "mgemm_run_mx4", "mgemm_linear_mx4",
-                 "mgemm_gated_mx4"):
+                 "mgemm_gated_mx4", "mgemm_set_mx4_kernel"):
         getattr(lib, name).restype = ci
     gated = [vp, ci, i64, i64, i64, vp, i64, vp, vp, i64]
     lib.mgemm_gated_workspace.argtypes = gated[1:] + [ci, ctypes.c_int32, ctypes.c_int32, pi64]
@@ -408,6 +409,15 @@ def mgemm_gated_mx4(h, M, N, K, X, ldx, xtype, Bg, SBg, Bu, SBu, ldb, ldsb, Z, l
                                 int(ldz), _enum(ztype, _DTYPE), _stream(stream))
     if st != MGEMM_SUCCESS:
         raise MgemmError(st, "mgemm_gated_mx4")
+
+
+def mgemm_set_mx4_kernel(h, kernel="auto", ksplit=0) -> None:
+    """Check hook: forces the kernel and split of the products in mgemm_linear_mx4
+    and mgemm_gated_mx4; "auto", 0: the library's choice."""
+    k = KERNELS.index(kernel) if isinstance(kernel, str) else int(kernel)
+    st = load().mgemm_set_mx4_kernel(h, k, int(ksplit))
+    if st != MGEMM_SUCCESS:
+        raise MgemmError(st, "mgemm_set_mx4_kernel")
 
 
 def mgemm_gated_workspace(layout, M, N, K, X, ldx, Wg, Wu, ldw, dtype, backward, stored) -> int:

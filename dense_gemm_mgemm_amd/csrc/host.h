@@ -56,6 +56,8 @@ struct mgemm_handle_s {
     unsigned long long* stamps;   // clock-stamp buffer (mgemm_set_clock_stamps), or null
     int64_t stamps_cap;           // workgroups it has room for
     mgemm_host::GatedTile gated_tile[3] = {};   // of the forward pair, dX and the weights' gradients
+    mgemm_kernel_t mx4_kernel = MGEMM_KERNEL_AUTO;   // forced on 4-bit products of values (mgemm_set_mx4_kernel),
+    int mx4_ksplit = 0;                              //   and its ranges
 };
 
 namespace mgemm_host {

@@ -30,6 +30,13 @@ bool valid_mx4(int64_t rows, int64_t K, int64_t ldq, int64_t lds) {
     return ldq >= max1(16 * nb) && lds >= max1(nb) && (rows == 0 || (ldq <= LIM / rows && lds <= LIM / rows));
 }
 
+// What mgemm_run_mx4 and mgemm_set_mx4_kernel accept.
+bool valid_kernel(mgemm_kernel_t kernel, int32_t ksplit) {
+    if (ksplit < 0 || ksplit > MGEMM_MAX_KSPLIT) return false;
+    if (kernel == MGEMM_KERNEL_AUTO) return ksplit == 0;
+    return kernel >= MGEMM_KERNEL_MX4_GENERAL && kernel <= MGEMM_KERNEL_MX4_MFMA_64;
+}
+
 Problem problem(mgemm_handle_t h, int64_t M, int64_t N, int64_t K, void* C, int64_t ldc, mgemm_dtype_t ctype) {
     Problem p{};
     p.M = M; p.N = N; p.K = K;
@@ -139,7 +146,8 @@ mgemm_status_t from_values(mgemm_handle_t h, Problem p, Mx4Args a, hipStream_t s
     // values (M = 1 .. 4, K = 4096: 10.6 us, from codes 9.0) and 7.6 at 65536;
     // a launch of its own adds 2.2 (M = 8: 11.6 us, from codes 9.4).
     constexpr int64_t IN_KERNEL = 20480;
-    if ((p.M <= 4 ? 4 : 16) * p.K <= IN_KERNEL && mgemm::mx4_skinny_supports(p, a))
+    const bool forced = h->mx4_kernel != MGEMM_KERNEL_AUTO;
+    if (!forced && (p.M <= 4 ? 4 : 16) * p.K <= IN_KERNEL && mgemm::mx4_skinny_supports(p, a))
         return status(mgemm::launch_mx4_skinny(p, a, s));
     // Codes and scales take the front half of the workspace, split-K partials the rest.
     const int64_t nb = mgemm::mx4_blocks(p.K), ldq = 16 * nb, lds = (nb + 15) / 16 * 16;
@@ -165,7 +173,7 @@ mgemm_status_t from_values(mgemm_handle_t h, Problem p, Mx4Args a, hipStream_t s
         p.C = C + m * p.ldc * cs;
         hipError_t e = mgemm::launch_quantize_mx4(p.M, p.K, X + m * a.ldx * es, a.ldx, a.xtype, q, ldq, sc, lds, s);
         if (e != hipSuccess) return MGEMM_ERR_HIP;
-        const mgemm_status_t st = launch(p, a, MGEMM_KERNEL_AUTO, 0, rest, s);
+        const mgemm_status_t st = launch(p, a, h->mx4_kernel, h->mx4_ksplit, rest, s);
         if (st != MGEMM_SUCCESS) return st;
     }
     return MGEMM_SUCCESS;
@@ -203,10 +211,7 @@ mgemm_status_t mgemm_run_mx4(mgemm_handle_t h, mgemm_kernel_t kernel, int32_t ks
                              const void* B, int64_t ldb, const void* SB, int64_t ldsb, float beta, void* C,
                              int64_t ldc, mgemm_dtype_t ctype, hipStream_t stream) {
     if (!h || M < 0 || N < 0 || K < 0 || !valid_dtype(ctype)) return MGEMM_ERR_INVALID_ARG;
-    if (ksplit < 0 || ksplit > MGEMM_MAX_KSPLIT || (kernel == MGEMM_KERNEL_AUTO && ksplit != 0))
-        return MGEMM_ERR_INVALID_ARG;
-    if (kernel != MGEMM_KERNEL_AUTO && (kernel < MGEMM_KERNEL_MX4_GENERAL || kernel > MGEMM_KERNEL_MX4_MFMA_64))
-        return MGEMM_ERR_INVALID_ARG;
+    if (!valid_kernel(kernel, ksplit)) return MGEMM_ERR_INVALID_ARG;
     if (!valid_mx4(M, K, lda, ldsa) || !valid_mx4(N, K, ldb, ldsb) || !valid_matrix(M, N, ldc))
         return MGEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return MGEMM_SUCCESS;
@@ -259,6 +264,13 @@ mgemm_status_t mgemm_gated_mx4(mgemm_handle_t h, int64_t M, int64_t N, int64_t K
     a.sb = (const uint8_t*)SBg; a.sb2 = (const uint8_t*)SBu; a.ldsb = ldsb;
     a.X = X; a.ldx = ldx; a.xtype = (int)xtype;
     return from_values(h, p, a, stream);
+}
+
+mgemm_status_t mgemm_set_mx4_kernel(mgemm_handle_t h, mgemm_kernel_t kernel, int32_t ksplit) {
+    if (!h || !valid_kernel(kernel, ksplit)) return MGEMM_ERR_INVALID_ARG;
+    h->mx4_kernel = kernel;
+    h->mx4_ksplit = ksplit;
+    return MGEMM_SUCCESS;
 }
 
 }  // extern "C"

@@ -556,6 +556,19 @@ mgemm_status_t mgemm_gated_mx4(mgemm_handle_t h, int64_t M, int64_t N, int64_t K
                                int64_t ldz, mgemm_dtype_t ztype, hipStream_t stream);
 
 /*
+ * mgemm_set_mx4_kernel -- check and measurement hook: later mgemm_linear_mx4 and
+ * mgemm_gated_mx4 calls through this handle quantise their activations in a
+ * launch of their own and multiply the codes with this kernel and split
+ * (`kernel` and `ksplit` as for mgemm_run_mx4; tests run every one).  The gated
+ * pair has no 256x256 and no 64x192 tile and takes the 192-wide ones with 96
+ * columns of each matrix.  MGEMM_KERNEL_AUTO with ksplit 0: the library's choice
+ * again.  A call that the forced kernel cannot run returns MGEMM_ERR_UNSUPPORTED.
+ * Errors: MGEMM_ERR_INVALID_ARG for a NULL handle, another kernel, or a split
+ * that mgemm_run_mx4 would not take.
+ */
+mgemm_status_t mgemm_set_mx4_kernel(mgemm_handle_t h, mgemm_kernel_t kernel, int32_t ksplit);
+
+/*
  * Training form of the gated block, FP16 and BF16: with X (M x K, row-major)
  * and two weights Wg and Wu,
  *     G = X Wg,  U = X Wu,  Z = SiLU(G) (.) U                       (forward)
