@@ -11,3 +11,9 @@ if ROOT not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (gfx950) GPU and the built HIP library")
     config.addinivalue_line("markers", "slow: long-running CPU test")
+
+
+def pytest_collectstart(collector):
+    # One module under both names that tests import it by: its compiled kernels are made once.
+    if "test_codegen" in sys.modules:
+        sys.modules.setdefault("tests.test_codegen", sys.modules["test_codegen"])
