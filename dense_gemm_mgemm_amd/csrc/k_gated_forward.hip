@@ -2,10 +2,10 @@
 // epilogue (Z, G, U) or the backward's (dG and dU from G, U computed again, and
 // dZ).
 //
-// Measured: 1024 x 1536 x 4096 BF16, weights in x out, 33 us (0.78 PFLOP/s): 192
+// Measured: 1024 x 1536 x 4096 BF16, weights in x out, 32 to 34 us (0.78 PFLOP/s): 192
 // workgroups of 128 tiles (256 tiles in 4 ranges 45), of which 30 in the tile
 // loop, bound by LDS (the weights' transposed reads move half the bytes per
-// clock).  777 x 1000 x 1001 FP16 with odd strides 19.8: 5.6 for the copies, 12.3
+// clock).  777 x 1000 x 1001 FP16 with odd strides 20.3: 5.6 for the copies, 12.7
 // for the product, of which 6.6 in the loop and the rest the first load and the
 // stores.
 #include "gated_tile.h"

@@ -22,8 +22,11 @@
 // selected by the instruction's byte select (0 in the first K-step, 2 in the
 // second).
 //
-// Measured: 8192 x 12288 x 4096 296 us (2.8 PFLOP/s), 8192 x 4096 x 12288 254 (3.2),
-// 4096^3 53; the gated pair 1024 x 12288 x 4096 84.  A slice of a 256x256 tile
+// Measured (codes given, calls back to back, over several cards): 8192 x 12288 x
+// 4096 296 to 303 us (2.7 to 2.8 PFLOP/s; in a kernel trace behind the quantisation of
+// 8192 rows 326 at least and 344 in the median), 8192 x 4096 x 12288 254 to 260 (3.2),
+// 4096^3 53 to 55; the gated pair 1024 x 12288 x 4096 84 to 88 (the call, with 6 of
+// quantisation, 90 to 94; traced 95 to 97).  A slice of a 256x256 tile
 // takes 2740 cycles for 1024 of matrix work (34.6 cycles an instruction alone):
 // 2580 without the scales' copies, 2230 without their LDS reads too, 2180 with
 // constant scales, so the codes' copies bound it and the scales add a quarter.
@@ -462,6 +465,10 @@ __global__ __launch_bounds__(NT) void k_mx4_reduce(Problem p, Mx4Args f) {
 // are multiples of 1/4 up to 36, so its sum is exact; both scales are applied to
 // the sum in one step, because a value times its own scale alone leaves FP32's
 // range from scale byte 253 on while the product may lie well inside it.
+//
+// Bound by its FP32 arithmetic, byte loads and, for few rows, idle CUs: 2880 x 2880
+// weights with packed scale rows of 90 bytes 235 / 247 / 335 us for 1 / 64 / 1024 rows,
+// the gated pair 673 / 650 / 600.
 constexpr int GT = 64;
 
 template <int CT, bool DUAL>

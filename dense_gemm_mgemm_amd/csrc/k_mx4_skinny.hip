@@ -10,8 +10,12 @@
 // next step's slices are requested before the present ones are multiplied.
 //
 // Bound by the weights' bytes and the launch: 1 / 4 / 16 x 12288 x 4096 from codes
-// 8.6 / 9.0 / 10.4 us (26.7 MB: 5.5 at a copy's rate), with the quantisation 10.6 /
-// 10.6 / 12.6; the gated pair of 4 rows 16.6 (53 MB).
+// 8.6 to 8.9 / 9.0 to 9.5 / 10.4 to 10.9 us (26.7 MB: 5.5 at a copy's rate), with the
+// quantisation 10.6 to 11.1 / 10.6 to 10.8 / 12.6 to 13.2; the gated pair of 4 rows
+// 16.6 to 17.2 (53 MB).  With the quantisation of up to 4 rows, the pair and two
+// column tiles hold 139 to 141 registers (16-bit X), so a CU has room for one
+// workgroup and not two, and 384 or 768 of them end in a round that is half empty;
+// from codes they hold 123.
 //
 // Few short rows are quantised here (RM rows at most, as 16-byte loads of
 // eight elements, four lanes to a block), each wave for its own slices through

@@ -65,10 +65,13 @@ constexpr Shape SHAPES[] = {{MGEMM_KERNEL_MX4_MFMA, 256, 256},
 
 // A tile's rate in the time model, from what a 128-element slice of it takes:
 // 64x192 0.5 us, 128x192 0.75 (0.58 for few rows, which stream the weights from
-// HBM whatever they compute), 256x192 1.0, 256x256 1.22 (300 x 5000 x 2000 on
-// 64 / 128 rows 12.4 / 16.8 us; 1000^3 8.8 / 11.7; 8192 x 12288 x 4096 on 64 / 128 /
-// 256 x 192 and 256 x 256 480 / 416 / 329 / 294; 48 x 12288 x 4096 whole 18.4, in
-// 4 ranges 12.3).
+// HBM whatever they compute), 256x192 1.0, 256x256 1.22.  Medians on three cards,
+// codes given: 300 x 5000 x 2000 on 64 / 128 rows 12.3 to 12.7 / 16.6 to 16.9 us;
+// 1000^3 8.3 to 8.8 / 11.1 to 11.4; 8192 x 12288 x 4096 on 64 / 128 / 256 x 192 and 256 x
+// 256 442 to 456 / 410 / 326 / 303; 48 x 12288 x 4096 whole 18.6, in 4 ranges 12.4 to
+// 13.6.  These are a few shapes, laid over a model of 16-bit products: it prices
+// the gated pair's splits too high (32 and 64 rows x 12288 x 4096 run whole in 30
+// us; in two ranges they take 22.6 and 24.6).
 double tile_speed(const Problem& p, int bn, int bm) {
     if (bm == 64) return 0.37;
     if (bm == 128) return p.M <= 128 ? 0.63 : 0.49;
@@ -100,10 +103,11 @@ Tile best_split(const Problem& p, int bn, int bm, const Workspace& ws, double* t
 // Predicted time (microseconds) of the decode kernel on codes: a launch, then
 // per 4096 columns (a 16-column workgroup on each CU; the gated pair has both
 // matrices') and 1024 elements of K (a slice for each wave) 0.023 us a row.
-// Measured on 4096 x 12288 weights: M = 17 / 32 / 48 / 64 12.0 / 14.2 / 20.5 /
-// 22.7 us, against 12.0 / 12.5 / 13.4 / 14.3 on 64-row tiles in 8 ranges; 12288
-// x 4096: M = 1 / 16 8.6 / 10.4 against 9.8 / 10.4 in 4; 40 x 1000 x 1000 6.0
-// against 8.0.
+// Medians on three cards, 4096 x 12288 weights: M = 17 / 32 / 48 / 64 12.2 to 12.5 /
+// 14.5 to 14.7 / 20.6 to 20.9 / 22.7 to 23.0 us, against 12.1 to 13.1 / 12.5 to 13.6 /
+// 13.3 to 14.3 / 14.3 to 15.1 on 64-row tiles in 8 ranges; 12288 x 4096: M = 1 / 16 8.7 to
+// 8.9 / 10.6 to 10.9 against 9.9 to 11.2 / 10.3 to 13.4 in 4; 40 x 1000 x 1000 6.0 to 9.3
+// against 7.9 to 9.9 (the host bounds the shortest).
 double skinny_us(const Problem& p) {
     const int64_t n = p.B2 != nullptr ? 2 * p.N : p.N;
     return 4.5 + (double)((n + 4095) / 4096) * (double)((p.K + 1023) / 1024) * 0.023 * (double)p.M;
@@ -143,8 +147,8 @@ mgemm_status_t from_values(mgemm_handle_t h, Problem p, Mx4Args a, hipStream_t s
     const int es = a.xtype == mgemm::F32 ? 4 : 2, cs = p.dtype == mgemm::F32 ? 4 : 2;
     // The decode kernel's own quantisation is repeated by every workgroup and
     // grows with the rows it has room for (4 or 16) times K: 1.6 us at 16384
-    // values (M = 1 .. 4, K = 4096: 10.6 us, from codes 9.0) and 7.6 at 65536;
-    // a launch of its own adds 2.2 (M = 8: 11.6 us, from codes 9.4).
+    // values (M = 1 .. 4, K = 4096: 10.6 to 10.8 us, from codes 8.7 to 9.5) and 7.6
+    // at 65536; a launch of its own adds 2.2 (M = 8: 11.6 to 12.4 us).
     constexpr int64_t IN_KERNEL = 20480;
     const bool forced = h->mx4_kernel != MGEMM_KERNEL_AUTO;
     if (!forced && (p.M <= 4 ? 4 : 16) * p.K <= IN_KERNEL && mgemm::mx4_skinny_supports(p, a))
